@@ -584,6 +584,147 @@ MOE_API int moe_backward(const moe_dims_t* dims, const moe_weights_t* w, const m
                          const uint16_t* dy, float alpha, float beta, const moe_grads_t* g, void* bwd_workspace,
                          moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * Slots sorted by expert from any routing, and rows moved there and back.
+ *
+ * moe_dispatch lays out the rows of what moe_route chose, from the ranks that call left in
+ * its workspace. These entry points take expert ids from anywhere (routing replayed from
+ * another run, another router) and rows of bf16, fp16 or fp32 of any width, and give the
+ * same layout: offsets, perm_tok and slot_row as moe_dispatch defines them, so that the
+ * grouped GEMMs (moe_expert_gate_up, moe_expert_down) run on it. An id outside [0, N) is a
+ * slot without an expert (a null copy, padding): it has no row, costs no memory traffic,
+ * and its weight is not read into any result.
+ *
+ * Row buffers: `rows` rows of d elements, ld >= d elements apart (ld is in elements). A row
+ * index at or past `rows` is skipped and sets MOE_ERR_DEVICE_BOUNDS in the status word at
+ * the start of `status` (any workspace of this library, or 256 bytes of the caller's; NULL:
+ * not recorded). Rows that no slot has are left as they were. Limits: 1 <= K <= 32,
+ * T * K < 2^31, 1 <= d <= 2^30. Inputs and outputs must not overlap, except where said. T = 0
+ * writes nothing but moe_sort_slots' counts and offsets. */
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_F16 = 1,
+  MOE_DTYPE_F32 = 2
+} moe_dtype_t;
+
+/* Workspace of moe_sort_slots in bytes (0 if the sizes are invalid): 256 + 4 N bytes per chunk of
+ * the slots, at most 148 chunks. Its first word is a status word that the sort clears. */
+MOE_API size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t N);
+
+/* Stable counting sort of the T*K slots by expert id (1 <= N <= 1024). ids [T, K] int32
+ * (id_bytes 4) or int64 (id_bytes 8). counts [N], offsets [N+1] (offsets[N] = R),
+ * slot_row [T, K] = offsets[id] + the slots before this one, in (token, slot) order, with the
+ * same id, or -1; perm_tok [T*K]: the token of each of the first R rows (the rest is left as
+ * it was). A token may carry the same expert twice: two rows. */
+MOE_API int moe_sort_slots(int32_t T, int32_t K, int32_t N, const void* ids, int32_t id_bytes,
+                           int32_t* counts, int32_t* offsets, int32_t* perm_tok, int32_t* slot_row,
+                           void* workspace, moe_stream_t stream);
+
+/* xs[slot_row[t,k]] = x[t]. */
+MOE_API int moe_permute(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype, const void* x,
+                        int64_t ldx, const int32_t* slot_row, void* xs, int64_t ldxs, void* status,
+                        moe_stream_t stream);
+
+/* Its gradient: dx[t] = base[t] + sum over the token's slots with a row, in slot order, of
+ * dxs[slot_row[t,k]]; fp32 sums, one rounding. base (another term of the input gradient) may
+ * be NULL (zero) or dx itself. */
+MOE_API int moe_permute_backward(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype,
+                                 const void* dxs, int64_t lddxs, const int32_t* slot_row, const void* base,
+                                 int64_t ldbase, void* dx, int64_t lddx, void* status, moe_stream_t stream);
+
+/* y[t] = base[t] + sum over the token's slots with a row, in slot order, of
+ * weights[t,k] * ys[slot_row[t,k]]; fp32 sums, one rounding. weights [T, K] fp32; base may be
+ * NULL (zero) or y itself. */
+MOE_API int moe_unpermute(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype, const void* ys,
+                          int64_t ldys, const float* weights, const int32_t* slot_row, const void* base,
+                          int64_t ldbase, void* y, int64_t ldy, void* status, moe_stream_t stream);
+
+/* Its gradient: dys[slot_row[t,k]] = weights[t,k] * dy[t] (one rounding) and dweights[t,k] =
+ * <dy[t], ys[slot_row[t,k]]> in fp32 (0 for a slot without a row). base's gradient is dy.
+ * dys may be NULL, or dweights and ys both. */
+MOE_API int moe_unpermute_backward(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype,
+                                   const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                                   const float* weights, const int32_t* slot_row, void* dys, int64_t lddys,
+                                   float* dweights, void* status, moe_stream_t stream);
+
+/* moe_unpermute_backward with ys as moe_checkpoint8 stored it: codes [rows, d], scales
+ * [rows, ceil(d / 32)]. */
+MOE_API int moe_unpermute_backward8(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype,
+                                    const void* dy, int64_t lddy, const int8_t* codes, const uint8_t* scales,
+                                    const float* weights, const int32_t* slot_row, void* dys, int64_t lddys,
+                                    float* dweights, void* status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Activations kept for the backward pass in 8 bits.
+ *
+ * A row is cut into blocks of 32 columns (the last one may be shorter). With m the largest
+ * magnitude of a block, E = max(floor(log2 m) - 6, -126), its elements x are held as the
+ * int8 code clamp(rint(x 2^-E), -127, 127) (half to even) and stand for code * 2^E; E + 127
+ * is the block's scale byte. The error is at most 2^(E-1) (about m / 128), for fp16 and fp32
+ * elements above 127.5 * 2^E less than 2^E. Values are exact in the type they came from. A
+ * block that holds an infinity or a NaN gets scale byte 255 and is restored as NaN.
+ *
+ * rows_used: device pointer to the number of rows in use (for a routed buffer offsets + N), or NULL
+ * for all of them; the rows behind it are neither read nor written. A number outside
+ * [0, rows] is clamped to it and sets MOE_ERR_DEVICE_BOUNDS in the status word (as above).
+ * codes and scales are dense. Limits: rows >= 0, rows * cols <= 2^60, 1 <= cols <= 2^30. */
+
+/* Scale bytes of a row of `cols` elements: ceil(cols / 32) (0 if cols < 1). */
+MOE_API size_t moe_checkpoint8_scales(int64_t cols);
+
+/* x [rows, cols] -> codes [rows, cols], scales [rows, ceil(cols / 32)]. */
+MOE_API int moe_checkpoint8(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t ldx,
+                            const int32_t* rows_used, int8_t* codes, uint8_t* scales, void* status,
+                            moe_stream_t stream);
+
+/* codes, scales -> x [rows, cols]. */
+MOE_API int moe_restore8(int64_t rows, int64_t cols, int32_t dtype, const int8_t* codes, const uint8_t* scales,
+                         const int32_t* rows_used, void* x, int64_t ldx, void* status, moe_stream_t stream);
+
+/* SwiGLU's backward from pre-activations z [rows, 2F] stored by moe_checkpoint8. With a, b the
+ * restored gate and up values, s = 1 / (1 + exp(-a)) and dh [rows, F] the gradient of h:
+ *   dz = [da | db], da = dh b s (1 + a (1 - s)), db = dh a s, and h = a s b
+ * (the activation recomputed, for the down projection's weight gradient; NULL: not written).
+ * packed != 0: z and dz in the order of moe_outputs_t.z (64-column panels of 64 gate then 64
+ * up columns; F a multiple of 64); 0: F gate columns, then F up columns. fp32 arithmetic, one
+ * rounding per output. dz, h and dh of one dtype. 2F <= 2^30. */
+MOE_API int moe_swiglu_backward8(int64_t rows, int64_t F, int32_t packed, int32_t dtype, const int8_t* codes,
+                                 const uint8_t* scales, const void* dh, int64_t lddh, const int32_t* rows_used,
+                                 void* dz, int64_t lddz, void* h, int64_t ldh, void* status,
+                                 moe_stream_t stream);
+
+/* What moe_backward_checkpoint8 reads of a forward (device pointers): the fields of
+ * moe_saved_t that are kept as they are, and in 8 bits the gate/up pre-activations z, z_shared
+ * and the routed outputs ys (each moe_checkpoint8 of the forward's buffer; the routed ones
+ * with rows_used = offsets + N). xs and h are not kept: the rows are gathered from x again and
+ * h is recomputed. */
+typedef struct moe_saved8 {
+  const uint16_t* x;          /* [T, d] bf16 layer input                              */
+  const float* logits;        /* [T, N+1+C+V]                                         */
+  const int32_t* topk_idx;    /* [T, K]                                               */
+  const float* topk_gate;     /* [T, K]                                               */
+  const int32_t* offsets;     /* [N+1]                                                */
+  const int32_t* slot_row;    /* [T, K]                                               */
+  const int32_t* counts_ext;  /* [N+M+C+V] slot counts over every data-parallel rank  */
+  int64_t t_total;            /* tokens over every data-parallel rank (>= T)          */
+  const int8_t* z_codes;      /* [R_cap, 2F]                                          */
+  const uint8_t* z_scales;    /* [R_cap, 2F / 32]                                     */
+  const int8_t* zs_codes;     /* [T, 2F_shared]                                       */
+  const uint8_t* zs_scales;   /* [T, 2F_shared / 32]                                  */
+  const int8_t* ys_codes;     /* [R_cap, d]                                           */
+  const uint8_t* ys_scales;   /* [R_cap, d / 32]                                      */
+} moe_saved8_t;
+
+/* Workspace of moe_backward_checkpoint8 in bytes (0 if dims are invalid): moe_backward's, and
+ * the buffers that hold xs, h and (C + V > 0) ys again. */
+MOE_API size_t moe_backward_checkpoint8_workspace_bytes(const moe_dims_t* dims);
+
+/* moe_backward from an 8-bit checkpoint: the same gradients of the layer at the stored
+ * pre-activations and outputs. */
+MOE_API int moe_backward_checkpoint8(const moe_dims_t* dims, const moe_weights_t* w, const moe_saved8_t* saved,
+                                     const uint16_t* dy, float alpha, float beta, const moe_grads_t* g,
+                                     void* workspace, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

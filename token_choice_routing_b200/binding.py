@@ -58,6 +58,15 @@ GRAD_FIELDS = ("dx", "dw_router", "dbias", "dtok_null_bias", "dw_gate", "dw_up",
                "dws_up", "dws_down", "dconst")
 
 
+SAVED8_FIELDS = ("x", "logits", "topk_idx", "topk_gate", "offsets", "slot_row", "counts_ext")
+SAVED8_CODES = ("z_codes", "z_scales", "zs_codes", "zs_scales", "ys_codes", "ys_scales")
+
+
+class Saved8(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in SAVED8_FIELDS] + [("t_total", C.c_int64)] +
+                [(n, C.c_void_p) for n in SAVED8_CODES])
+
+
 class Grads(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in GRAD_FIELDS]
 
@@ -67,7 +76,7 @@ def _load() -> C.CDLL:
         raise ImportError(f"CUDA library not built: {LIB_PATH} is missing "
                           "(run python -m token_choice_routing_b200.build)")
     lib = C.CDLL(LIB_PATH)
-    vp, i32, sz = C.c_void_p, C.c_int, C.c_size_t
+    vp, i32, i64, sz = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
     pd = C.POINTER(Dims)
     sig = {
         "moe_abi_version": (i32, []),
@@ -115,6 +124,20 @@ def _load() -> C.CDLL:
         "moe_expert_wgrad_down": (i32, [pd, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_expert_dgrad_gate_up": (i32, [pd, vp, vp, vp, vp, vp, vp, vp, vp]),
         "moe_expert_wgrad_gate_up": (i32, [pd, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "moe_sort_workspace_bytes": (sz, [i32, i32, i32]),
+        "moe_sort_slots": (i32, [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp]),
+        "moe_permute": (i32, [i32, i32, i64, i32, i32, vp, i64, vp, vp, i64, vp, vp]),
+        "moe_permute_backward": (i32, [i32, i32, i64, i32, i32, vp, i64, vp, vp, i64, vp, i64, vp, vp]),
+        "moe_unpermute": (i32, [i32, i32, i64, i32, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp]),
+        "moe_unpermute_backward": (i32, [i32, i32, i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp]),
+        "moe_unpermute_backward8": (i32, [i32, i32, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp]),
+        "moe_checkpoint8_scales": (sz, [i64]),
+        "moe_checkpoint8": (i32, [i64, i64, i32, vp, i64, vp, vp, vp, vp, vp]),
+        "moe_restore8": (i32, [i64, i64, i32, vp, vp, vp, vp, i64, vp, vp]),
+        "moe_swiglu_backward8": (i32, [i64, i64, i32, i32, vp, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp]),
+        "moe_backward_checkpoint8_workspace_bytes": (sz, [pd]),
+        "moe_backward_checkpoint8": (i32, [pd, C.POINTER(Weights), C.POINTER(Saved8), vp, C.c_float, C.c_float,
+                                           C.POINTER(Grads), vp, vp]),
         "moe_backward": (i32, [pd, C.POINTER(Weights), C.POINTER(Saved), vp, C.c_float, C.c_float,
                                C.POINTER(Grads), vp, vp]),
     }
@@ -393,3 +416,248 @@ def expert_swiglu_backward_saved(dm, offsets, z, z_shared, bws, stream=None):
     _check("moe_expert_swiglu_backward_saved",
            LIB.moe_expert_swiglu_backward_saved(C.byref(dm), _p(offsets), _p(z), _p(z_shared), _p(bws),
                                                 _stream(stream)))
+
+
+def backward_checkpoint8_workspace_bytes(dm: Dims) -> int:
+    return int(LIB.moe_backward_checkpoint8_workspace_bytes(C.byref(dm)))
+
+
+def backward_checkpoint8(dm, weights: Weights, saved: Saved8, dy, alpha, beta, grads: Grads, ws, stream=None):
+    """moe_backward from the 8-bit checkpoint in ``saved``."""
+    _check("moe_backward_checkpoint8",
+           LIB.moe_backward_checkpoint8(C.byref(dm), C.byref(weights), C.byref(saved), _p(dy), float(alpha),
+                                        float(beta), C.byref(grads), _p(ws), _stream(stream)))
+
+
+# ------------------------------------------------------ slots from any routing, 8-bit checkpoints
+#
+# These calls take tensors of several types and row strides, so unlike the calls above they
+# check types and shapes here (ValueError) before the library checks sizes (MoEError). Row
+# tensors are two-dimensional with adjacent elements in a row; any row stride of at least the
+# width will do. Everything else is contiguous.
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, dev: int):
+    """(data pointer, row stride) of a [rows, cols] row tensor."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, not {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    if ld < cols:
+        if rows > 1:
+            raise ValueError(f"rows of {name} must not overlap")
+        ld = cols
+    return t.data_ptr(), ld
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype: torch.dtype, dev: int) -> int:
+    """Data pointer of a contiguous tensor."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {name}")
+    return t.data_ptr()
+
+
+def _status(ws: Optional[torch.Tensor], dev: int):
+    """Pointer of the workspace whose status word records device-side errors, or None."""
+    if ws is None:
+        return None
+    if ws.get_device() != dev:
+        raise ValueError("ws must be a CUDA tensor on the current device")
+    if not ws.is_contiguous() or ws.numel() * ws.element_size() < 4 or ws.data_ptr() % 4:
+        raise ValueError("ws must be a workspace: contiguous, at least a status word, 4-byte aligned")
+    return ws.data_ptr()
+
+
+def _two_d(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    return t.shape
+
+
+def sort_workspace_bytes(T: int, K: int, N: int) -> int:
+    return int(LIB.moe_sort_workspace_bytes(int(T), int(K), int(N)))
+
+
+def sort_slots(ids, N, counts, offsets, perm_tok, slot_row, ws, stream=None):
+    """Slots sorted by expert: ids [T, K] int32 or int64 (outside [0, N): no expert) ->
+    counts [N], offsets [N+1], perm_tok [T*K], slot_row [T, K], all int32. ws: at least
+    ``sort_workspace_bytes(T, K, N)`` bytes."""
+    T, K = _two_d(ids, "ids")
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    if ids.dtype != i32 and ids.dtype != torch.int64:
+        raise ValueError(f"ids must be int32 or int64, not {ids.dtype}")
+    need = LIB.moe_sort_workspace_bytes(T, K, N)
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
+        raise ValueError(f"ws must hold sort_workspace_bytes = {need} bytes")
+    _check("moe_sort_slots",
+           LIB.moe_sort_slots(T, K, N, _dense(ids, "ids", (T, K), ids.dtype, dev), ids.element_size(),
+                              _dense(counts, "counts", (N,), i32, dev), _dense(offsets, "offsets", (N + 1,), i32, dev),
+                              _dense(perm_tok, "perm_tok", (T * K,), i32, dev),
+                              _dense(slot_row, "slot_row", (T, K), i32, dev), _status(ws, dev), _stream(stream)))
+
+
+def permute(x, slot_row, xs, ws=None, stream=None):
+    """xs[slot_row[t, k]] = x[t] for every slot with a row; the other rows of xs stay as they are."""
+    T, d = _two_d(x, "x")
+    K = _two_d(slot_row, "slot_row")[1]
+    rows = _two_d(xs, "xs")[0]
+    dev = torch.cuda.current_device()
+    dt = _dtype(x, "x")
+    px, ldx = _rows(x, "x", T, d, x.dtype, dev)
+    po, ldo = _rows(xs, "xs", rows, d, x.dtype, dev)
+    _check("moe_permute", LIB.moe_permute(T, K, rows, d, dt, px, ldx,
+                                          _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
+                                          _status(ws, dev), _stream(stream)))
+
+
+def permute_backward(dxs, slot_row, dx, base=None, ws=None, stream=None):
+    """dx[t] = base[t] + sum_k dxs[slot_row[t, k]]; base None is zero, base may be dx itself."""
+    T, d = _two_d(dx, "dx")
+    K = _two_d(slot_row, "slot_row")[1]
+    rows = _two_d(dxs, "dxs")[0]
+    dev = torch.cuda.current_device()
+    dt = _dtype(dx, "dx")
+    pi, ldi = _rows(dxs, "dxs", rows, d, dx.dtype, dev)
+    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, dx.dtype, dev)
+    po, ldo = _rows(dx, "dx", T, d, dx.dtype, dev)
+    _check("moe_permute_backward",
+           LIB.moe_permute_backward(T, K, rows, d, dt, pi, ldi,
+                                    _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
+                                    _status(ws, dev), _stream(stream)))
+
+
+def unpermute(ys, weights, slot_row, y, base=None, ws=None, stream=None):
+    """y[t] = base[t] + sum_k weights[t, k] ys[slot_row[t, k]]; base None is zero, base may be y
+    itself."""
+    T, d = _two_d(y, "y")
+    K = _two_d(slot_row, "slot_row")[1]
+    rows = _two_d(ys, "ys")[0]
+    dev = torch.cuda.current_device()
+    dt = _dtype(y, "y")
+    pi, ldi = _rows(ys, "ys", rows, d, y.dtype, dev)
+    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, y.dtype, dev)
+    po, ldo = _rows(y, "y", T, d, y.dtype, dev)
+    _check("moe_unpermute",
+           LIB.moe_unpermute(T, K, rows, d, dt, pi, ldi, _dense(weights, "weights", (T, K), torch.float32, dev),
+                             _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
+                             _status(ws, dev), _stream(stream)))
+
+
+def unpermute_backward(dy, ys, weights, slot_row, dys, dweights, ws=None, stream=None):
+    """dys[slot_row[t, k]] = weights[t, k] dy[t] and dweights[t, k] = <dy[t], ys[slot_row[t, k]]>
+    (fp32 [T, K]). dys may be None, or ys and dweights both."""
+    T, d = _two_d(dy, "dy")
+    K = _two_d(slot_row, "slot_row")[1]
+    if dys is None and ys is None:
+        raise ValueError("dys and ys cannot both be None")
+    if (ys is None) != (dweights is None):
+        raise ValueError("ys and dweights go together")
+    rows = _two_d(ys if dys is None else dys, "ys" if dys is None else "dys")[0]
+    dev = torch.cuda.current_device()
+    dt = _dtype(dy, "dy")
+    f32 = torch.float32
+    pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
+    pi, ldi = (None, 0) if ys is None else _rows(ys, "ys", rows, d, dy.dtype, dev)
+    po, ldo = (None, 0) if dys is None else _rows(dys, "dys", rows, d, dy.dtype, dev)
+    _check("moe_unpermute_backward",
+           LIB.moe_unpermute_backward(T, K, rows, d, dt, pt, ldt, pi, ldi, _dense(weights, "weights", (T, K), f32, dev),
+                                      _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
+                                      None if dweights is None else _dense(dweights, "dweights", (T, K), f32, dev),
+                                      _status(ws, dev), _stream(stream)))
+
+
+def unpermute_backward8(dy, codes, scales, weights, slot_row, dys, dweights, ws=None, stream=None):
+    """``unpermute_backward`` with ys as ``checkpoint8`` stored it. dys may be None."""
+    T, d = _two_d(dy, "dy")
+    K = _two_d(slot_row, "slot_row")[1]
+    rows = _two_d(codes, "codes")[0]
+    dev = torch.cuda.current_device()
+    dt = _dtype(dy, "dy")
+    f32 = torch.float32
+    pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
+    po, ldo = (None, 0) if dys is None else _rows(dys, "dys", rows, d, dy.dtype, dev)
+    _check("moe_unpermute_backward8",
+           LIB.moe_unpermute_backward8(T, K, rows, d, dt, pt, ldt, _dense(codes, "codes", (rows, d), torch.int8, dev),
+                                       _dense(scales, "scales", (rows, (d + 31) // 32), torch.uint8, dev),
+                                       _dense(weights, "weights", (T, K), f32, dev),
+                                       _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
+                                       _dense(dweights, "dweights", (T, K), f32, dev), _status(ws, dev),
+                                       _stream(stream)))
+
+
+def checkpoint8_scales(cols: int) -> int:
+    return int(LIB.moe_checkpoint8_scales(int(cols)))
+
+
+def _used(rows_used, dev: int):
+    if rows_used is None:
+        return None
+    if rows_used.numel() != 1:
+        raise ValueError("rows_used must be one int32")
+    return _dense(rows_used, "rows_used", tuple(rows_used.shape), torch.int32, dev)
+
+
+def checkpoint8(x, codes, scales, rows_used=None, ws=None, stream=None):
+    """x [rows, cols] stored in 8 bits: codes [rows, cols] int8, scales [rows, ceil(cols / 32)]
+    uint8. rows_used (one int32 on the device, e.g. ``offsets[N:]``): the rows in use."""
+    rows, cols = _two_d(x, "x")
+    dev = torch.cuda.current_device()
+    dt = _dtype(x, "x")
+    px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
+    _check("moe_checkpoint8",
+           LIB.moe_checkpoint8(rows, cols, dt, px, ldx, _used(rows_used, dev),
+                               _dense(codes, "codes", (rows, cols), torch.int8, dev),
+                               _dense(scales, "scales", (rows, (cols + 31) // 32), torch.uint8, dev),
+                               _status(ws, dev), _stream(stream)))
+
+
+def restore8(codes, scales, x, rows_used=None, ws=None, stream=None):
+    """The activation that ``checkpoint8`` stored, into x [rows, cols]."""
+    rows, cols = _two_d(x, "x")
+    dev = torch.cuda.current_device()
+    dt = _dtype(x, "x")
+    px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
+    _check("moe_restore8",
+           LIB.moe_restore8(rows, cols, dt, _dense(codes, "codes", (rows, cols), torch.int8, dev),
+                            _dense(scales, "scales", (rows, (cols + 31) // 32), torch.uint8, dev),
+                            _used(rows_used, dev), px, ldx, _status(ws, dev), _stream(stream)))
+
+
+def swiglu_backward8(codes, scales, dh, dz, h, packed=True, rows_used=None, ws=None, stream=None):
+    """SwiGLU's backward from pre-activations stored by ``checkpoint8`` (codes [rows, 2F]): dz
+    [rows, 2F] from dh [rows, F], and the activation h [rows, F] recomputed (None: not written).
+    packed: columns in the layer's order (64-column panels of gate, then up), else F gate
+    columns, then F up columns."""
+    rows, F = _two_d(dh, "dh")
+    dev = torch.cuda.current_device()
+    dt = _dtype(dh, "dh")
+    pg, ldg = _rows(dh, "dh", rows, F, dh.dtype, dev)
+    pz, ldz = _rows(dz, "dz", rows, 2 * F, dh.dtype, dev)
+    ph, ldh = (None, 0) if h is None else _rows(h, "h", rows, F, dh.dtype, dev)
+    _check("moe_swiglu_backward8",
+           LIB.moe_swiglu_backward8(rows, F, 1 if packed else 0, dt,
+                                    _dense(codes, "codes", (rows, 2 * F), torch.int8, dev),
+                                    _dense(scales, "scales", (rows, (2 * F + 31) // 32), torch.uint8, dev),
+                                    pg, ldg, _used(rows_used, dev), pz, ldz, ph, ldh, _status(ws, dev),
+                                    _stream(stream)))

@@ -19,10 +19,11 @@ static int check_pp_inputs(const moe_dims_t* d, const int32_t* topk_idx, const u
 
 // The five expert GEMMs. With w->w_router set, the router's input gradient ds W_r (from the
 // split ds that the router backward left in the workspace) is added to dx_shared inside the
-// shared expert's gate/up dgrad.
+// shared expert's gate/up dgrad. With s8 set, the pre-activations come from its 8-bit blocks,
+// and h and h_shared of sv are written from them before the weight gradient reads them.
 static int expert_ffn_bwd(const moe_dims_t& d, const moe_weights_t* w, const moe_saved_t* sv, const uint16_t* dys,
                           const uint16_t* dy, uint16_t* dxs, uint16_t* dx_shared, const moe_grads_t* g, void* ws,
-                          cudaStream_t st) {
+                          cudaStream_t st, const moe_saved8_t* s8 = nullptr) {
   const BwdLayout L = bwd_layout(d);
   uint32_t* status = ws_ptr<uint32_t>(ws, L.hdr);
   uint16_t* dh = ws_ptr<uint16_t>(ws, L.dh);
@@ -38,7 +39,13 @@ static int expert_ffn_bwd(const moe_dims_t& d, const moe_weights_t* w, const moe
     MOE_CHECK(launch_router_split2(d, w->w_router, w2, st));
   }
   MOE_CHECK(launch_dgrad_down(d, sv->offsets, dys, dy, w->w_down, w->shared_down, dh, dhs, status, st));
-  if (sv->z && sv->z_shared)  // training mode: pre-activations saved by the forward
+  if (s8) {
+    MOE_CHECK(launch_swiglu_backward8((long long)d.T * d.K, d.F, 1, MOE_DTYPE_BF16, s8->z_codes, s8->z_scales, dh, d.F,
+                                      sv->offsets + d.N, dz, 2 * d.F, const_cast<uint16_t*>(sv->h), d.F, status, st));
+    MOE_CHECK(launch_swiglu_backward8(d.T, d.F_shared, 1, MOE_DTYPE_BF16, s8->zs_codes, s8->zs_scales, dhs, d.F_shared,
+                                      nullptr, dzs, 2 * d.F_shared, const_cast<uint16_t*>(sv->h_shared), d.F_shared,
+                                      status, st));
+  } else if (sv->z && sv->z_shared)  // training mode: pre-activations saved by the forward
     MOE_CHECK(launch_swiglu_bwd_saved(d, sv->offsets, sv->z, sv->z_shared, dh, dhs, dz, dzs, status, st));
   else
     MOE_CHECK(launch_swiglu_backward(d, sv->offsets, sv->xs, sv->x, w->gate_up, w->shared_gate_up, dh, dhs, dz, dzs,
@@ -68,6 +75,74 @@ static bool saved_ok(const moe_saved_t* s, const moe_dims_t* d) {
 
 static bool expert_grads_ok(const moe_grads_t* g) {
   return g && g->dw_gate && g->dw_up && g->dw_down && g->dws_gate && g->dws_up && g->dws_down;
+}
+
+static bool weights_ok(const moe_weights_t* w, const moe_dims_t* d) {
+  return w && w->w_router && w->gate_up && w->w_down && w->shared_gate_up && w->shared_down &&
+         (d->V == 0 || w->const_vectors);
+}
+
+static bool saved8_ok(const moe_saved8_t* s, const moe_dims_t* d) {
+  return s && s->x && s->logits && s->topk_idx && s->topk_gate && s->offsets && s->slot_row && s->counts_ext &&
+         s->t_total >= (int64_t)d->T && s->t_total > 0 && s->z_codes && s->z_scales && s->zs_codes && s->zs_scales &&
+         s->ys_codes && s->ys_scales;
+}
+
+// Workspace of the backward from an 8-bit checkpoint: moe_backward's, then the gathered rows,
+// the activations and (with MoE++ experts, whose combine backward reads them in bf16) the
+// routed outputs.
+struct Ckpt8Layout {
+  size_t xs, h, hs, ys, total;
+};
+static Ckpt8Layout ckpt8_layout(const moe_dims_t& d) {
+  const size_t rcap = (size_t)d.T * d.K, T = (size_t)d.T;
+  Ckpt8Layout L{};
+  size_t o = align_up(bwd_layout(d).total, 256);
+  L.xs = o; o = align_up(o + 2 * rcap * d.d, 256);
+  L.h = o; o = align_up(o + 2 * rcap * d.F, 256);
+  L.hs = o; o = align_up(o + 2 * T * d.F_shared, 256);
+  L.ys = o; o = align_up(o + (d.C + d.V > 0 ? 2 * rcap * d.d : 0), 256);
+  L.total = o;
+  return L;
+}
+
+// The whole backward; with s8, from an 8-bit checkpoint: saved's xs, h, h_shared and ys are
+// then workspace buffers that this call fills.
+static int backward_run(const moe_dims_t& d, const moe_weights_t* w, const moe_saved_t* saved, const moe_saved8_t* s8,
+                        const uint16_t* dy, float alpha, float beta, const moe_grads_t* g, void* ws,
+                        cudaStream_t st) {
+  const BwdLayout L = bwd_layout(d);
+  uint32_t* status = ws_ptr<uint32_t>(ws, L.hdr);
+  uint16_t* dys = ws_ptr<uint16_t>(ws, L.dys);
+  uint16_t* dxs = ws_ptr<uint16_t>(ws, L.dxs);
+  float* dg = ws_ptr<float>(ws, L.dg);
+  float* ds = ws_ptr<float>(ws, L.ds);
+  MOE_CHECK(cuda_status(cudaMemsetAsync(status, 0, sizeof(uint32_t), st)));
+  const long long rcap = (long long)d.T * d.K;
+  if (s8) {  // the gathered rows again
+    MOE_CHECK(launch_spread(d.T, d.K, rcap, d.d, MOE_DTYPE_BF16, saved->x, d.d, nullptr, 0, nullptr, nullptr,
+                            saved->slot_row, const_cast<uint16_t*>(saved->xs), d.d, nullptr, status, st));
+    if (saved->ys)
+      MOE_CHECK(launch_restore8(rcap, d.d, MOE_DTYPE_BF16, s8->ys_codes, s8->ys_scales, saved->offsets + d.N,
+                                const_cast<uint16_t*>(saved->ys), d.d, status, st));
+  }
+  if (s8 && !saved->ys)  // every slot is a real expert or a null copy: the outputs straight from their codes
+    MOE_CHECK(launch_spread(d.T, d.K, rcap, d.d, MOE_DTYPE_BF16, dy, d.d, s8->ys_codes, d.d, s8->ys_scales,
+                            saved->topk_gate, saved->slot_row, dys, d.d, dg, status, st));
+  else
+    MOE_CHECK(launch_combine_bwd(d, dy, saved->ys, saved->topk_gate, saved->slot_row, saved->topk_idx, saved->x,
+                                 w->const_vectors, dys, dg, status, st));
+  MOE_CHECK(launch_router_bwd(d, saved->logits, saved->topk_idx, saved->topk_gate, dg, saved->counts_ext,
+                              (long long)saved->t_total, alpha, beta, ds, g->dtok_null_bias,
+                              ws_ptr<uint16_t>(ws, L.dsplit), ws_ptr<float>(ws, L.bpart), st));
+  MOE_CHECK(router_wgrad(d, saved->x, g->dw_router, g->dbias, ws, st));
+  // the shared expert's (and the router's) input gradient goes straight into dx; the input
+  // gradient gather then adds the routed and copy-expert terms in place, skipping the tokens
+  // that have none
+  MOE_CHECK(expert_ffn_bwd(d, w, saved, dys, dy, dxs, g->dx, g, ws, st, s8));
+  MOE_CHECK(launch_input_grad(d, g->dx, dxs, saved->slot_row, saved->topk_idx, saved->topk_gate, dy, g->dx, status,
+                              st));
+  return launch_const_grad(d, saved->topk_idx, saved->topk_gate, dy, g->dconst, st);
 }
 
 extern "C" {
@@ -229,35 +304,43 @@ int moe_backward(const moe_dims_t* dims, const moe_weights_t* w, const moe_saved
                  float alpha, float beta, const moe_grads_t* g, void* bwd_workspace, moe_stream_t stream) {
   MOE_CHECK(check_dims(dims));
   if (dims->T == 0) return MOE_OK;
-  if (!w || !w->w_router || !w->gate_up || !w->w_down || !w->shared_gate_up || !w->shared_down)
-    return MOE_ERR_INVALID_ARG;
-  if (dims->V > 0 && !w->const_vectors) return MOE_ERR_INVALID_ARG;
+  if (!weights_ok(w, dims)) return MOE_ERR_INVALID_ARG;
   if (!saved_ok(saved, dims) || !dy || !expert_grads_ok(g) || !g->dx || !g->dw_router || !bwd_workspace)
     return MOE_ERR_INVALID_ARG;
   if (dims->V > 0 && !g->dconst) return MOE_ERR_INVALID_ARG;
+  return backward_run(*dims, w, saved, nullptr, dy, alpha, beta, g, bwd_workspace, S(stream));
+}
+
+size_t moe_backward_checkpoint8_workspace_bytes(const moe_dims_t* dims) {
+  if (check_dims(dims) != MOE_OK) return 0;
+  return ckpt8_layout(*dims).total;
+}
+
+int moe_backward_checkpoint8(const moe_dims_t* dims, const moe_weights_t* w, const moe_saved8_t* s8,
+                             const uint16_t* dy, float alpha, float beta, const moe_grads_t* g, void* workspace,
+                             moe_stream_t stream) {
+  MOE_CHECK(check_dims(dims));
+  if (dims->T == 0) return MOE_OK;
+  if (!weights_ok(w, dims) || !saved8_ok(s8, dims) || !dy || !expert_grads_ok(g) || !g->dx || !g->dw_router ||
+      !workspace)
+    return MOE_ERR_INVALID_ARG;
+  if (dims->V > 0 && !g->dconst) return MOE_ERR_INVALID_ARG;
   const moe_dims_t& d = *dims;
-  const cudaStream_t st = S(stream);
-  const BwdLayout L = bwd_layout(d);
-  void* ws = bwd_workspace;
-  uint32_t* status = ws_ptr<uint32_t>(ws, L.hdr);
-  uint16_t* dys = ws_ptr<uint16_t>(ws, L.dys);
-  uint16_t* dxs = ws_ptr<uint16_t>(ws, L.dxs);
-  float* dg = ws_ptr<float>(ws, L.dg);
-  float* ds = ws_ptr<float>(ws, L.ds);
-  MOE_CHECK(cuda_status(cudaMemsetAsync(status, 0, sizeof(uint32_t), st)));
-  MOE_CHECK(launch_combine_bwd(d, dy, saved->ys, saved->topk_gate, saved->slot_row, saved->topk_idx, saved->x,
-                               w->const_vectors, dys, dg, status, st));
-  MOE_CHECK(launch_router_bwd(d, saved->logits, saved->topk_idx, saved->topk_gate, dg, saved->counts_ext,
-                              (long long)saved->t_total, alpha, beta, ds, g->dtok_null_bias,
-                              ws_ptr<uint16_t>(ws, L.dsplit), ws_ptr<float>(ws, L.bpart), st));
-  MOE_CHECK(router_wgrad(d, saved->x, g->dw_router, g->dbias, ws, st));
-  // the shared expert's (and the router's) input gradient goes straight into dx; the input
-  // gradient gather then adds the routed and copy-expert terms in place, skipping the tokens
-  // that have none
-  MOE_CHECK(expert_ffn_bwd(d, w, saved, dys, dy, dxs, g->dx, g, ws, st));
-  MOE_CHECK(launch_input_grad(d, g->dx, dxs, saved->slot_row, saved->topk_idx, saved->topk_gate, dy, g->dx, status,
-                              st));
-  return launch_const_grad(d, saved->topk_idx, saved->topk_gate, dy, g->dconst, st);
+  const Ckpt8Layout L = ckpt8_layout(d);
+  moe_saved_t sv{};
+  sv.x = s8->x;
+  sv.logits = s8->logits;
+  sv.topk_idx = s8->topk_idx;
+  sv.topk_gate = s8->topk_gate;
+  sv.offsets = s8->offsets;
+  sv.slot_row = s8->slot_row;
+  sv.counts_ext = s8->counts_ext;
+  sv.t_total = s8->t_total;
+  sv.xs = ws_ptr<uint16_t>(workspace, L.xs);
+  sv.h = ws_ptr<uint16_t>(workspace, L.h);
+  sv.h_shared = ws_ptr<uint16_t>(workspace, L.hs);
+  sv.ys = d.C + d.V > 0 ? ws_ptr<uint16_t>(workspace, L.ys) : nullptr;
+  return backward_run(d, w, &sv, s8, dy, alpha, beta, g, workspace, S(stream));
 }
 
 }  // extern "C"

@@ -322,6 +322,27 @@ int launch_router_wgrad_tc(const moe_dims_t& d, const uint16_t* dsplit, const ui
 int launch_router_split2(const moe_dims_t& d, const float* w_router, uint16_t* w2, cudaStream_t st);
 int launch_router_wgrad_reduce(const moe_dims_t& d, const float* part, int nchunk, const float* bpart, float* dw,
                                float* dbias, cudaStream_t st);
+// Slots sorted by expert, rows moved there and back (slots.cu), and activations in 8 bits
+// (ckpt8.cu). status: a status word, or null.
+size_t sort_workspace_bytes(int T, int K, int N);
+int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_t* counts, int32_t* offsets,
+                      int32_t* perm_tok, int32_t* slot_row, void* ws, cudaStream_t st);
+// out[t] = base[t] + sum_k w[t,k] rows_in[slot_row[t,k]] (w null: ones; base null: zero)
+int launch_collect(int T, int K, long long rows, int d, int dtype, const void* rows_in, long long ldr, const float* w,
+                   const int32_t* slot_row, const void* base, long long ldb, void* out, long long ldo,
+                   uint32_t* status, cudaStream_t st);
+// rows_out[slot_row[t,k]] = w[t,k] tok[t] (w null: ones; rows_out null: not written) and, with dw,
+// dw[t,k] = <tok[t], rows_in[slot_row[t,k]]>; with scales, rows_in holds 8-bit codes
+int launch_spread(int T, int K, long long rows, int d, int dtype, const void* tok, long long ldt, const void* rows_in,
+                  long long ldr, const uint8_t* scales, const float* w, const int32_t* slot_row, void* rows_out,
+                  long long ldro, float* dw, uint32_t* status, cudaStream_t st);
+int launch_checkpoint8(long long rows, int cols, int dtype, const void* x, long long ldx, const int32_t* used,
+                       int8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t st);
+int launch_restore8(long long rows, int cols, int dtype, const int8_t* codes, const uint8_t* scales,
+                    const int32_t* used, void* x, long long ldx, uint32_t* status, cudaStream_t st);
+int launch_swiglu_backward8(long long rows, int F, int packed, int dtype, const int8_t* codes, const uint8_t* scales,
+                            const void* dh, long long lddh, const int32_t* used, void* dz, long long lddz, void* h,
+                            long long ldh, uint32_t* status, cudaStream_t st);
 int launch_combine_bwd(const moe_dims_t& d, const uint16_t* dy, const uint16_t* ys, const float* topk_gate,
                        const int32_t* slot_row, const int32_t* topk_idx, const uint16_t* x,
                        const uint16_t* const_vectors, uint16_t* dys, float* dg, uint32_t* status, cudaStream_t st);

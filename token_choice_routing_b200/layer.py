@@ -178,8 +178,10 @@ class MoENullLayer:
         out["workspace"] = torch.empty((max(B.workspace_bytes(self.dims(T)), 256),), dtype=torch.uint8, device=dev)
         return out
 
-    def alloc_grads(self, T: int) -> Dict[str, torch.Tensor]:
-        """Gradient buffers and the backward workspace for a T-token backward."""
+    def alloc_grads(self, T: int, checkpoint8: bool = False) -> Dict[str, torch.Tensor]:
+        """Gradient buffers and the backward workspace for a T-token backward
+        (checkpoint8=True: for ``backward_checkpoint8``, whose workspace also holds the rows
+        and activations that it rebuilds)."""
         dev, d, N, F, Fs = self.device, self.d, self.N, self.F, self.F_shared
         rows = N + 1 + self.C + self.V
         bf, f32 = torch.bfloat16, torch.float32
@@ -196,8 +198,8 @@ class MoENullLayer:
             dws_down=torch.empty((d, Fs), dtype=bf, device=dev),
             dconst=torch.empty((self.V, d), dtype=f32, device=dev) if self.V else None,
         )
-        g["workspace"] = torch.empty((max(B.backward_workspace_bytes(self.dims(T)), 256),), dtype=torch.uint8,
-                                     device=dev)
+        need = (B.backward_checkpoint8_workspace_bytes if checkpoint8 else B.backward_workspace_bytes)(self.dims(T))
+        g["workspace"] = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
         return g
 
     def saved(self, x: torch.Tensor, out: Dict[str, torch.Tensor], counts_ext: Optional[torch.Tensor] = None,
@@ -226,6 +228,187 @@ class MoENullLayer:
         sv = self.saved(x, out, counts_ext, t_total)
         g = B.Grads(*[None if grads.get(n) is None else grads[n].data_ptr() for n in B.GRAD_FIELDS])
         B.backward(self.dims(T), self._weights, sv, dy, alpha, beta, g, grads["workspace"], stream)
+        return grads
+
+    # ------------------------------------------------------------ training with 8-bit checkpoints
+
+    def alloc_checkpoint8(self, T: int) -> Dict[str, torch.Tensor]:
+        """What one forward leaves for its backward in 8 bits: the gate/up pre-activations and
+        the routed outputs as codes with a scale byte per 32 columns, and the routing as it is.
+        Per routed slot that is (2 F + d) 33/32 bytes in the place of the 6 F + 4 d that z, h, xs
+        and ys take in bf16, which the layers of a model then share as scratch
+        (``alloc(T, save_preact=True)`` once)."""
+        dev, d, N, M, K, F, Fs = self.device, self.d, self.N, self.M, self.K, self.F, self.F_shared
+        R, T1 = max(T * K, 1), max(T, 1)
+        i32, f32, i8, u8 = torch.int32, torch.float32, torch.int8, torch.uint8
+        ck = dict(
+            logits=torch.empty((T, N + 1 + self.C + self.V), dtype=f32, device=dev),
+            topk_idx=torch.empty((T, K), dtype=i32, device=dev),
+            topk_gate=torch.empty((T, K), dtype=f32, device=dev),
+            offsets=torch.empty((N + 1,), dtype=i32, device=dev),
+            slot_row=torch.empty((T, K), dtype=i32, device=dev),
+            counts_ext=torch.empty((N + M + self.C + self.V,), dtype=i32, device=dev),
+        )
+        for name, rows, cols in (("z", R, 2 * F), ("zs", T1, 2 * Fs), ("ys", R, d)):
+            ck[name + "_codes"] = torch.empty((rows, cols), dtype=i8, device=dev)
+            ck[name + "_scales"] = torch.empty((rows, B.checkpoint8_scales(cols)), dtype=u8, device=dev)
+        return ck
+
+    def forward_checkpoint8(self, x: torch.Tensor, tok_null_bias: Optional[torch.Tensor],
+                            out: Dict[str, torch.Tensor], ck: Dict[str, torch.Tensor],
+                            stream=None) -> Dict[str, torch.Tensor]:
+        """The forward, keeping for the backward only ``ck`` (``alloc_checkpoint8``) and x. ``out``
+        (``alloc(T, save_preact=True)``) is scratch that the next layer's forward may use; its
+        buffers of the routing are left alone and the checkpoint's taken. Returns the outputs as
+        ``forward`` does."""
+        T = x.shape[0]
+        R = T * self.K
+        if out.get("z") is None or out.get("xs") is None or out["z"].shape[0] < R or out["y"].shape[0] < T:
+            raise ValueError("an 8-bit checkpoint needs out from alloc(T, save_preact=True)")
+        if ck["slot_row"].shape[0] < T:
+            raise ValueError(f"the checkpoint holds {ck['slot_row'].shape[0]} tokens, not {T}")
+        o = dict(out)
+        o.update({n: ck[n] for n in B.SAVED8_FIELDS if n != "x"})
+        self.forward(x, tok_null_bias, o, stream)
+        if T > 0:
+            ws, used = o["workspace"], o["offsets"][self.N:]
+            B.checkpoint8(o["z"][:R], ck["z_codes"][:R], ck["z_scales"][:R], used, ws, stream)
+            B.checkpoint8(o["z_shared"][:T], ck["zs_codes"][:T], ck["zs_scales"][:T], None, ws, stream)
+            B.checkpoint8(o["ys"][:R], ck["ys_codes"][:R], ck["ys_scales"][:R], used, ws, stream)
+        return o
+
+    def backward_checkpoint8(self, x: torch.Tensor, ck: Dict[str, torch.Tensor], dy: torch.Tensor,
+                             alpha: float = 2e-2, beta: float = 1e-3,
+                             grads: Optional[Dict[str, torch.Tensor]] = None,
+                             counts_ext: Optional[torch.Tensor] = None, t_total: Optional[int] = None,
+                             stream=None) -> Dict[str, torch.Tensor]:
+        """``backward`` from what ``forward_checkpoint8`` kept: the gradients at the stored
+        pre-activations and outputs (``moe_backward_checkpoint8``). grads: from
+        ``alloc_grads(T, checkpoint8=True)``."""
+        T = x.shape[0]
+        dm = self.dims(T)
+        if ck["slot_row"].shape[0] < T:
+            raise ValueError(f"the checkpoint holds {ck['slot_row'].shape[0]} tokens, not {T}")
+        if grads is None:
+            grads = self.alloc_grads(T, checkpoint8=True)
+        if grads["workspace"].numel() < B.backward_checkpoint8_workspace_bytes(dm):
+            raise ValueError("grads must come from alloc_grads(T, checkpoint8=True)")
+        sv = B.Saved8()
+        for n in B.SAVED8_FIELDS + B.SAVED8_CODES:
+            setattr(sv, n, x.data_ptr() if n == "x" else ck[n].data_ptr())
+        if counts_ext is not None:
+            sv.counts_ext = counts_ext.data_ptr()
+        sv.t_total = int(T if t_total is None else t_total)
+        g = B.Grads(*[None if grads.get(n) is None else grads[n].data_ptr() for n in B.GRAD_FIELDS])
+        B.backward_checkpoint8(dm, self._weights, sv, dy, alpha, beta, g, grads["workspace"], stream)
+        return grads
+
+    # ------------------------------------------------------- the experts on a given routing
+
+    def _routed_dims(self, T: int, K: int) -> B.Dims:
+        if self.C + self.V > 0:
+            raise ValueError("a given routing chooses among the N real experts: C and V must be 0")
+        dm = self.dims(T)
+        dm.K, dm.M = K, max(self.M, K - self.N)  # the pool plays no part: only T, K and the real experts
+        return dm
+
+    def _check_tokens(self, name: str, t: torch.Tensor, T: int):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, self.d) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bfloat16 of shape {(T, self.d)}, not {t.dtype} "
+                             f"{tuple(t.shape)}")
+
+    def alloc_routed(self, T: int, K: int) -> Dict[str, torch.Tensor]:
+        """Buffers of ``forward_routed`` for T tokens of K slots each."""
+        dev, d, N, F, Fs = self.device, self.d, self.N, self.F, self.F_shared
+        R, T1 = max(T * K, 1), max(T, 1)
+        i32, bf = torch.int32, torch.bfloat16
+        out = dict(
+            counts=torch.empty((N,), dtype=i32, device=dev),
+            offsets=torch.empty((N + 1,), dtype=i32, device=dev),
+            perm_tok=torch.empty((T * K,), dtype=i32, device=dev),
+            slot_row=torch.empty((T, K), dtype=i32, device=dev),
+            xs=torch.empty((R, d), dtype=bf, device=dev),
+            h=torch.empty((R, F), dtype=bf, device=dev),
+            h_shared=torch.empty((T1, Fs), dtype=bf, device=dev),
+            ys=torch.empty((R, d), dtype=bf, device=dev),
+            y=torch.empty((T1, d), dtype=bf, device=dev),
+        )
+        out["workspace"] = torch.empty((max(B.sort_workspace_bytes(T, K, N), 256),), dtype=torch.uint8, device=dev)
+        return out
+
+    def forward_routed(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_gate: torch.Tensor,
+                       out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
+        """y = E_shared(x) + sum_k topk_gate[t, k] E_{topk_idx[t, k]}(x) with the routing given by
+        the caller (replayed from another run, or another router's) in the place of this layer's
+        router. topk_idx [T, K] int32 or int64, K <= 16; an index outside [0, N) is a slot
+        without an expert, whose gate is not used. topk_gate [T, K] fp32. Buffers from
+        ``alloc_routed(T, K)``."""
+        T, K = topk_idx.shape
+        dm = self._routed_dims(T, K)
+        if B.check_dims(dm) != B.OK:
+            raise B.MoEError("moe_check_dims", B.check_dims(dm))
+        self._check_tokens("x", x, T)
+        if out is None:
+            out = self.alloc_routed(T, K)
+        ws = out["workspace"]
+        B.sort_slots(topk_idx, self.N, out["counts"], out["offsets"], out["perm_tok"], out["slot_row"], ws, stream)
+        if T == 0:
+            return out
+        y = out["y"]
+        B.permute(x, out["slot_row"], out["xs"], ws, stream)
+        B.expert_gate_up(dm, out["xs"], x, out["offsets"], self.gate_up, self.shared_gate_up, out["h"],
+                         out["h_shared"], ws, stream)
+        B.expert_down(dm, out["offsets"], out["h"], out["h_shared"], self.w_down, self.shared_down, out["ys"], y, ws,
+                      stream)
+        B.unpermute(out["ys"], topk_gate, out["slot_row"], y, base=y, ws=ws, stream=stream)
+        return out
+
+    def alloc_routed_grads(self, T: int, K: int) -> Dict[str, torch.Tensor]:
+        """Gradient buffers, row buffers and the workspace of ``backward_routed``."""
+        dev, d, N, F, Fs = self.device, self.d, self.N, self.F, self.F_shared
+        R, T1 = max(T * K, 1), max(T, 1)
+        bf = torch.bfloat16
+        g = dict(
+            dx=torch.empty((T1, d), dtype=bf, device=dev),
+            dgate=torch.empty((T, K), dtype=torch.float32, device=dev),
+            dw_gate=torch.empty((N, F, d), dtype=bf, device=dev),
+            dw_up=torch.empty((N, F, d), dtype=bf, device=dev),
+            dw_down=torch.empty((N, d, F), dtype=bf, device=dev),
+            dws_gate=torch.empty((Fs, d), dtype=bf, device=dev),
+            dws_up=torch.empty((Fs, d), dtype=bf, device=dev),
+            dws_down=torch.empty((d, Fs), dtype=bf, device=dev),
+            dys=torch.empty((R, d), dtype=bf, device=dev),
+            dxs=torch.empty((R, d), dtype=bf, device=dev),
+        )
+        need = B.backward_workspace_bytes(self._routed_dims(T, K))
+        g["workspace"] = torch.empty((max(need, 256),), dtype=torch.uint8, device=dev)
+        return g
+
+    def backward_routed(self, x: torch.Tensor, topk_gate: torch.Tensor, out: Dict[str, torch.Tensor],
+                        dy: torch.Tensor, grads: Optional[Dict[str, torch.Tensor]] = None,
+                        stream=None) -> Dict[str, torch.Tensor]:
+        """Gradients of <y, dy> after ``forward_routed``: dx, the experts' and the shared expert's
+        weights, and dgate [T, K] for whatever computed the gates. The router has no part in it.
+        Buffers from ``alloc_routed_grads(T, K)``."""
+        T, K = topk_gate.shape
+        dm = self._routed_dims(T, K)
+        self._check_tokens("x", x, T)
+        self._check_tokens("dy", dy, T)
+        if grads is None:
+            grads = self.alloc_routed_grads(T, K)
+        if T == 0:
+            return grads
+        ws = grads["workspace"]
+        ptr = lambda t: t.data_ptr()
+        B.clear_device_status(ws, stream)
+        B.unpermute_backward(dy, out["ys"], topk_gate, out["slot_row"], grads["dys"], grads["dgate"], ws, stream)
+        w = B.Weights(gate_up=ptr(self.gate_up), w_down=ptr(self.w_down), shared_gate_up=ptr(self.shared_gate_up),
+                      shared_down=ptr(self.shared_down))
+        sv = B.Saved(x=ptr(x), offsets=ptr(out["offsets"]), xs=ptr(out["xs"]), h=ptr(out["h"]),
+                     h_shared=ptr(out["h_shared"]))
+        g = B.Grads(**{n: ptr(grads[n]) for n in B.GRAD_FIELDS if n in grads})
+        B.expert_ffn_backward(dm, w, sv, grads["dys"], dy, grads["dxs"], grads["dx"], g, ws, stream)
+        B.permute_backward(grads["dxs"], out["slot_row"], grads["dx"], base=grads["dx"], ws=ws, stream=stream)
         return grads
 
     def alloc_host_pipeline(self, chunk: int, nsets: int = 2) -> Dict[str, object]:
