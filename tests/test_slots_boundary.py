@@ -163,7 +163,7 @@ def cpu_as_device(monkeypatch):
     """The checks run before any pointer is used: with CPU tensors taken for the current
     device's, every call below must raise in the binding or be refused by the library."""
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
-    monkeypatch.setattr(B, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(B, "_raw_stream", lambda stream, dev: None)
 
 
 def z(*shape, dtype=torch.bfloat16):

@@ -448,33 +448,43 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 
 def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, dev: int):
     """(data pointer, row stride) of a [rows, cols] row tensor."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must have shape {(rows, cols)}, not {tuple(t.shape)}")
-    ld, inner = t.stride()
+    if t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == dev:
+        ld, inner = t.stride()
+        if inner == 1 and ld >= cols:
+            return t.data_ptr(), ld
+    _placed(t, name, (rows, cols), dtype, dev)
     if inner != 1 and cols > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    if ld < cols:
-        if rows > 1:
-            raise ValueError(f"rows of {name} must not overlap")
-        ld = cols
-    return t.data_ptr(), ld
+    if ld < cols and rows > 1:
+        raise ValueError(f"rows of {name} must not overlap")
+    return t.data_ptr(), max(ld, cols)
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype: torch.dtype, dev: int) -> int:
     """Data pointer of a contiguous tensor."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _placed(t, name, shape, dtype, dev)
+    raise ValueError(f"expected a contiguous {name}")
+
+
+def _placed(t: torch.Tensor, name: str, shape, dtype: torch.dtype, dev: int):
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"expected a contiguous {name}")
-    return t.data_ptr()
+
+
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle, without building a stream object for the current one (3 us a call,
+    a quarter of a decode-sized call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _status(ws: Optional[torch.Tensor], dev: int):
@@ -503,7 +513,7 @@ def sort_slots(ids, N, counts, offsets, perm_tok, slot_row, ws, stream=None):
     counts [N], offsets [N+1], perm_tok [T*K], slot_row [T, K], all int32. ws: at least
     ``sort_workspace_bytes(T, K, N)`` bytes."""
     T, K = _two_d(ids, "ids")
-    dev = torch.cuda.current_device()
+    dev = _device()
     i32 = torch.int32
     if ids.dtype != i32 and ids.dtype != torch.int64:
         raise ValueError(f"ids must be int32 or int64, not {ids.dtype}")
@@ -514,7 +524,7 @@ def sort_slots(ids, N, counts, offsets, perm_tok, slot_row, ws, stream=None):
            LIB.moe_sort_slots(T, K, N, _dense(ids, "ids", (T, K), ids.dtype, dev), ids.element_size(),
                               _dense(counts, "counts", (N,), i32, dev), _dense(offsets, "offsets", (N + 1,), i32, dev),
                               _dense(perm_tok, "perm_tok", (T * K,), i32, dev),
-                              _dense(slot_row, "slot_row", (T, K), i32, dev), _status(ws, dev), _stream(stream)))
+                              _dense(slot_row, "slot_row", (T, K), i32, dev), _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def permute(x, slot_row, xs, ws=None, stream=None):
@@ -522,13 +532,13 @@ def permute(x, slot_row, xs, ws=None, stream=None):
     T, d = _two_d(x, "x")
     K = _two_d(slot_row, "slot_row")[1]
     rows = _two_d(xs, "xs")[0]
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(x, "x")
     px, ldx = _rows(x, "x", T, d, x.dtype, dev)
     po, ldo = _rows(xs, "xs", rows, d, x.dtype, dev)
     _check("moe_permute", LIB.moe_permute(T, K, rows, d, dt, px, ldx,
                                           _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
-                                          _status(ws, dev), _stream(stream)))
+                                          _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def permute_backward(dxs, slot_row, dx, base=None, ws=None, stream=None):
@@ -536,7 +546,7 @@ def permute_backward(dxs, slot_row, dx, base=None, ws=None, stream=None):
     T, d = _two_d(dx, "dx")
     K = _two_d(slot_row, "slot_row")[1]
     rows = _two_d(dxs, "dxs")[0]
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(dx, "dx")
     pi, ldi = _rows(dxs, "dxs", rows, d, dx.dtype, dev)
     pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, dx.dtype, dev)
@@ -544,7 +554,7 @@ def permute_backward(dxs, slot_row, dx, base=None, ws=None, stream=None):
     _check("moe_permute_backward",
            LIB.moe_permute_backward(T, K, rows, d, dt, pi, ldi,
                                     _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
-                                    _status(ws, dev), _stream(stream)))
+                                    _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def unpermute(ys, weights, slot_row, y, base=None, ws=None, stream=None):
@@ -553,7 +563,7 @@ def unpermute(ys, weights, slot_row, y, base=None, ws=None, stream=None):
     T, d = _two_d(y, "y")
     K = _two_d(slot_row, "slot_row")[1]
     rows = _two_d(ys, "ys")[0]
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(y, "y")
     pi, ldi = _rows(ys, "ys", rows, d, y.dtype, dev)
     pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, y.dtype, dev)
@@ -561,7 +571,7 @@ def unpermute(ys, weights, slot_row, y, base=None, ws=None, stream=None):
     _check("moe_unpermute",
            LIB.moe_unpermute(T, K, rows, d, dt, pi, ldi, _dense(weights, "weights", (T, K), torch.float32, dev),
                              _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
-                             _status(ws, dev), _stream(stream)))
+                             _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def unpermute_backward(dy, ys, weights, slot_row, dys, dweights, ws=None, stream=None):
@@ -574,7 +584,7 @@ def unpermute_backward(dy, ys, weights, slot_row, dys, dweights, ws=None, stream
     if (ys is None) != (dweights is None):
         raise ValueError("ys and dweights go together")
     rows = _two_d(ys if dys is None else dys, "ys" if dys is None else "dys")[0]
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(dy, "dy")
     f32 = torch.float32
     pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
@@ -584,7 +594,7 @@ def unpermute_backward(dy, ys, weights, slot_row, dys, dweights, ws=None, stream
            LIB.moe_unpermute_backward(T, K, rows, d, dt, pt, ldt, pi, ldi, _dense(weights, "weights", (T, K), f32, dev),
                                       _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
                                       None if dweights is None else _dense(dweights, "dweights", (T, K), f32, dev),
-                                      _status(ws, dev), _stream(stream)))
+                                      _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def unpermute_backward8(dy, codes, scales, weights, slot_row, dys, dweights, ws=None, stream=None):
@@ -592,7 +602,7 @@ def unpermute_backward8(dy, codes, scales, weights, slot_row, dys, dweights, ws=
     T, d = _two_d(dy, "dy")
     K = _two_d(slot_row, "slot_row")[1]
     rows = _two_d(codes, "codes")[0]
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(dy, "dy")
     f32 = torch.float32
     pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
@@ -603,7 +613,7 @@ def unpermute_backward8(dy, codes, scales, weights, slot_row, dys, dweights, ws=
                                        _dense(weights, "weights", (T, K), f32, dev),
                                        _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
                                        _dense(dweights, "dweights", (T, K), f32, dev), _status(ws, dev),
-                                       _stream(stream)))
+                                       _raw_stream(stream, dev)))
 
 
 def checkpoint8_scales(cols: int) -> int:
@@ -622,26 +632,26 @@ def checkpoint8(x, codes, scales, rows_used=None, ws=None, stream=None):
     """x [rows, cols] stored in 8 bits: codes [rows, cols] int8, scales [rows, ceil(cols / 32)]
     uint8. rows_used (one int32 on the device, e.g. ``offsets[N:]``): the rows in use."""
     rows, cols = _two_d(x, "x")
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(x, "x")
     px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
     _check("moe_checkpoint8",
            LIB.moe_checkpoint8(rows, cols, dt, px, ldx, _used(rows_used, dev),
                                _dense(codes, "codes", (rows, cols), torch.int8, dev),
                                _dense(scales, "scales", (rows, (cols + 31) // 32), torch.uint8, dev),
-                               _status(ws, dev), _stream(stream)))
+                               _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def restore8(codes, scales, x, rows_used=None, ws=None, stream=None):
     """The activation that ``checkpoint8`` stored, into x [rows, cols]."""
     rows, cols = _two_d(x, "x")
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(x, "x")
     px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
     _check("moe_restore8",
            LIB.moe_restore8(rows, cols, dt, _dense(codes, "codes", (rows, cols), torch.int8, dev),
                             _dense(scales, "scales", (rows, (cols + 31) // 32), torch.uint8, dev),
-                            _used(rows_used, dev), px, ldx, _status(ws, dev), _stream(stream)))
+                            _used(rows_used, dev), px, ldx, _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def swiglu_backward8(codes, scales, dh, dz, h, packed=True, rows_used=None, ws=None, stream=None):
@@ -650,7 +660,7 @@ def swiglu_backward8(codes, scales, dh, dz, h, packed=True, rows_used=None, ws=N
     packed: columns in the layer's order (64-column panels of gate, then up), else F gate
     columns, then F up columns."""
     rows, F = _two_d(dh, "dh")
-    dev = torch.cuda.current_device()
+    dev = _device()
     dt = _dtype(dh, "dh")
     pg, ldg = _rows(dh, "dh", rows, F, dh.dtype, dev)
     pz, ldz = _rows(dz, "dz", rows, 2 * F, dh.dtype, dev)
@@ -660,4 +670,4 @@ def swiglu_backward8(codes, scales, dh, dz, h, packed=True, rows_used=None, ws=N
                                     _dense(codes, "codes", (rows, 2 * F), torch.int8, dev),
                                     _dense(scales, "scales", (rows, (2 * F + 31) // 32), torch.uint8, dev),
                                     pg, ldg, _used(rows_used, dev), pz, ldz, ph, ldh, _status(ws, dev),
-                                    _stream(stream)))
+                                    _raw_stream(stream, dev)))

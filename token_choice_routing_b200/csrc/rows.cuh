@@ -19,6 +19,24 @@ inline bool rows_aligned16(const void* p, int64_t ld, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ((uint64_t)ld * (uint64_t)bytes) % 16u == 0;
 }
 
+// Division of n < 2^31 by a fixed 1 <= d < 2^31 as a multiplication (Granlund and Montgomery):
+// with 2^(l-1) < d <= 2^l and m = ceil(2^(31+l) / d), floor(n / d) = floor(n m / 2^(31+l)).
+struct FastDiv {
+  uint32_t d, m, shift;
+  FastDiv() : d(1), m(0), shift(0) {}
+  explicit FastDiv(uint32_t div) : d(div), m(0), shift(0) {
+    int l = 0;
+    while ((1ull << l) < div) ++l;
+    if (l > 0) {
+      m = (uint32_t)(((1ull << (31 + l)) + div - 1) / div);
+      shift = (uint32_t)(l - 1);
+    }
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return d == 1u ? n : __umulhi(n, m) >> shift; }
+#endif
+};
+
 #ifdef __CUDACC__
 
 template <typename T>
@@ -40,41 +58,88 @@ __device__ __forceinline__ __half float_to_elem<__half>(float v) { return __floa
 template <>
 __device__ __forceinline__ float float_to_elem<float>(float v) { return v; }
 
-// V consecutive elements: one 16-byte access when V fills it, an element access when V = 1.
+// V consecutive elements as they lie in memory: four words by one 16-byte access, or one element
+// (V = 1). The words stay whole until they are used: element arrays made the compiler split and
+// rejoin them, at twice the kernel's time for the 16-bit types.
 template <typename T, int V>
 struct Piece {
-  T e[V];
+  static_assert(V * sizeof(T) == 16, "a piece is 16 bytes or one element");
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_own(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = w; }
+  __device__ __forceinline__ void get(float (&v)[V]) const;
+  __device__ __forceinline__ void set(const float (&v)[V]);
+};
+template <typename T>
+struct Piece<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(p); }
+  __device__ __forceinline__ void load_own(const T* p) { w = *p; }  // p may be written by this kernel
+  __device__ __forceinline__ void zero() { w = float_to_elem<T>(0.f); }
+  __device__ __forceinline__ void store(T* p) const { *p = w; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = elem_to_float<T>(w); }
+  __device__ __forceinline__ void set(const float (&v)[1]) { w = float_to_elem<T>(v[0]); }
 };
 
-template <typename T, int V>
-__device__ __forceinline__ Piece<T, V> load_piece(const T* p) {
-  Piece<T, V> r;
-  if constexpr (V * sizeof(T) == 16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    memcpy(r.e, &v, 16);
-  } else {
-    static_assert(V == 1, "a piece is 16 bytes or one element");
-    r.e[0] = *p;
-  }
-  return r;
+// Two 16-bit elements of a word as fp32 and back.
+template <typename T>
+__device__ __forceinline__ float2 word_to_float2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 word_to_float2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16lo(w), bf16hi(w));
+}
+template <>
+__device__ __forceinline__ float2 word_to_float2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t float2_to_word(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t float2_to_word<__nv_bfloat16>(float a, float b) { return pack_bf16x2(a, b); }
+template <>
+__device__ __forceinline__ uint32_t float2_to_word<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <typename T, int V>
-__device__ __forceinline__ Piece<T, V> zero_piece() {
-  Piece<T, V> r;
-  memset(r.e, 0, sizeof(r.e));
-  return r;
+__device__ __forceinline__ void Piece<T, V>::get(float (&v)[V]) const {
+  if constexpr (V == 4) {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+  } else {
+    const float2 a = word_to_float2<T>(w.x), b = word_to_float2<T>(w.y), c = word_to_float2<T>(w.z),
+                 d = word_to_float2<T>(w.w);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void Piece<T, V>::set(const float (&v)[V]) {
+  if constexpr (V == 4)
+    w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    w = make_uint4(float2_to_word<T>(v[0], v[1]), float2_to_word<T>(v[2], v[3]), float2_to_word<T>(v[4], v[5]),
+                   float2_to_word<T>(v[6], v[7]));
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& r) {
-  if constexpr (V * sizeof(T) == 16) {
-    uint4 v;
-    memcpy(&v, r.e, 16);
-    *reinterpret_cast<uint4*>(p) = v;
-  } else {
-    *p = r.e[0];
-  }
+// Four int8 codes of a word as fp32: each byte, its sign bit flipped, becomes the low mantissa
+// byte of 2^23 + (code + 128), from which 2^23 + 128 is taken off exactly. One byte permute and
+// one addition a code, where the integer conversion runs at a fraction of that rate.
+__device__ __forceinline__ void codes_to_float(uint32_t word, float (&v)[4]) {
+  const uint32_t u = word ^ 0x80808080u;
+  v[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540)) - 8388736.f;
+  v[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541)) - 8388736.f;
+  v[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7542)) - 8388736.f;
+  v[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7543)) - 8388736.f;
+}
+
+// 2^E of a scale byte, NaN for byte 255.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
 #endif  // __CUDACC__

@@ -205,8 +205,22 @@ int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_
 }
 
 // ---------------------------------------------------------------------------------------
-// Row movement. One warp per token; its lanes hold the token's slots (lane k: slot k).
+// Row movement. Rows are read and written in pieces of V elements, consecutive pieces by
+// consecutive lanes: 16 bytes where the layout allows it, single elements otherwise. A warp
+// takes one token's columns [c0, c0 + 32 V NV), NV pieces a lane, and its lanes hold the token's
+// slots (lane k: slot k), compacted four at a time so that all their pieces are in flight
+// together.
 constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+// Pieces a lane holds of each row (NV) and CTAs a multiprocessor (at most 64 registers a thread). With
+// four slots at a time a lane has 8 row pieces and 2 of the token in flight: 32 warps x 5 KB cover
+// the latency of HBM. Measured at T = 65536, d = 2048, K = 8, bf16 (unpermute): NV 2 with 4 CTAs
+// 245 us (6.6 TB/s, the copy rate), NV 1 with 6 or 8 CTAs 271 and 248 us, NV 2 with 3 CTAs 266 us.
+constexpr int kVecPieces = 2;
+constexpr int kRowCtas = 4;
+// Single elements (odd widths, unaligned rows): 8 a lane; 4 a lane measured 122 against 97 us
+// (T = 16384, d = 1537, K = 8, bf16).
+constexpr int kElemPieces = 8;
 
 // The slot's row, -1 for none. A row past the buffer is skipped and recorded.
 __device__ __forceinline__ int slot_row_checked(const int32_t* slot_row, long long t, int k, int K, long long rows,
@@ -232,105 +246,268 @@ struct RowArgs {
   uint32_t* status;
   long long ldt, ldr, ldto, ldro, rows;
   int T, K, d;
+  int items;           // T * chunks: a warp's work is one chunk of one token
+  FastDiv chunks;      // chunks of a token: ceil(d / (32 V NV))
 };
 
-// tok_out[t] = tok[t] + sum_k w[t,k] rows_in[slot_row[t,k]], fp32 sums in slot order.
-template <typename E, int V>
-__global__ void __launch_bounds__(kRowThreads) collect_kernel(RowArgs a) {
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const int wpb = kRowThreads / 32;
-  for (long long t = (long long)blockIdx.x * wpb + (threadIdx.x >> 5); t < a.T; t += (long long)gridDim.x * wpb) {
-    const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
-    const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
-    const unsigned has = __ballot_sync(0xffffffffu, row >= 0);
-    const E* base = static_cast<const E*>(a.tok);
-    E* out = static_cast<E*>(a.tok_out) + t * a.ldto;
-    for (int c0 = 0; c0 < a.d; c0 += 32 * V) {  // warp-uniform trip count
-      const int c = c0 + lane * V;
-      const bool ok = c < a.d;
-      float acc[V];
-      const Piece<E, V> b = (base && ok) ? load_piece<E, V>(base + t * a.ldt + c) : zero_piece<E, V>();
+// The next (up to four) slots with a row, from the mask m: their rows (-1 past the end) and weights.
+__device__ __forceinline__ void next_slots(unsigned& m, int row, float w, int (&r)[4], float (&wk)[4]) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = elem_to_float<E>(b.e[j]);
-      for (unsigned m = has; m; m &= m - 1u) {
-        const int k = __ffs(m) - 1;
-        const long long r = __shfl_sync(0xffffffffu, row, k);
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        if (ok) {
-          const Piece<E, V> v = load_piece<E, V>(static_cast<const E*>(a.rows_in) + r * a.ldr + c);
-#pragma unroll
-          for (int j = 0; j < V; ++j) acc[j] = fmaf(wk, elem_to_float<E>(v.e[j]), acc[j]);
-        }
-      }
-      if (ok) {
-        Piece<E, V> o;
-#pragma unroll
-        for (int j = 0; j < V; ++j) o.e[j] = float_to_elem<E>(acc[j]);
-        store_piece<E, V>(out + c, o);
-      }
-    }
+  for (int u = 0; u < 4; ++u) {
+    const int k = m ? __ffs(m) - 1 : 0;
+    r[u] = __shfl_sync(0xffffffffu, row, k);
+    wk[u] = __shfl_sync(0xffffffffu, w, k);
+    if (m == 0u) r[u] = -1;
+    m &= m - 1u;
   }
 }
 
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
+// tok_out[t] = tok[t] + sum_k w[t,k] rows_in[slot_row[t,k]], fp32 sums in slot order.
+template <typename E, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs a) {
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (item >= (uint32_t)a.items) return;
+  const long long t = a.chunks.quotient(item);
+  const int c0 = (int)(item - (uint32_t)t * a.chunks.d) * (32 * V * NV) + lane * V;
+  const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
+  const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
+  const E* base = static_cast<const E*>(a.tok) + t * a.ldt;
+  const E* rows_in = static_cast<const E*>(a.rows_in);
+  float acc[NV][V];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = c0 + v * 32 * V;
+    Piece<E, V> b;
+    b.zero();
+    if (a.tok && c < a.d) b.load_own(base + c);
+    b.get(acc[v]);
+  }
+  unsigned m = __ballot_sync(0xffffffffu, row >= 0);
+  while (m) {
+    int r[4];
+    float wk[4];
+    next_slots(m, row, w, r, wk);
+    Piece<E, V> p[4][NV];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const E* src = rows_in + (long long)r[u] * a.ldr;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = c0 + v * 32 * V;
+        p[u][v].zero();
+        if (r[u] >= 0 && c < a.d) p[u][v].load(src + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (r[u] < 0) continue;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[V];
+        p[u][v].get(f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[v][j] = fmaf(wk[u], f[j], acc[v][j]);
+      }
+    }
+  }
+  E* out = static_cast<E*>(a.tok_out) + t * a.ldto;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = c0 + v * 32 * V;
+    if (c >= a.d) continue;
+    Piece<E, V> o;
+    o.set(acc[v]);
+    o.store(out + c);
+  }
 }
 
-// rows_out[slot_row[t,k]] = w[t,k] tok[t], and with dw, dw[t,k] = <tok[t], rows_in[slot_row[t,k]]>
-// (fp32 sums per lane, then a fixed shuffle tree; 0 for a slot without a row).
-template <typename E, int V, bool DOT, bool CODES>
+// rows_out[slot_row[t,k]] = w[t,k] tok[t] (w null: a copy).
+template <typename E, int V, int NV>
 __global__ void __launch_bounds__(kRowThreads) spread_kernel(RowArgs a) {
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
-  const int wpb = kRowThreads / 32;
-  const int nb = (a.d + 31) / 32;
-  for (long long t = (long long)blockIdx.x * wpb + (threadIdx.x >> 5); t < a.T; t += (long long)gridDim.x * wpb) {
-    const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
-    const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
-    const E* src = static_cast<const E*>(a.tok) + t * a.ldt;
-    float mydw = 0.f;
-    for (unsigned m = __ballot_sync(0xffffffffu, row >= 0); m; m &= m - 1u) {
-      const int k = __ffs(m) - 1;
-      const long long r = __shfl_sync(0xffffffffu, row, k);
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      float dot = 0.f;
-      for (int c = lane * V; c < a.d; c += 32 * V) {
-        const Piece<E, V> v = load_piece<E, V>(src + c);
-        if (a.rows_out) {
-          Piece<E, V> o = v;
-          if (a.w) {
+  const uint32_t item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (item >= (uint32_t)a.items) return;
+  const long long t = a.chunks.quotient(item);
+  const int c0 = (int)(item - (uint32_t)t * a.chunks.d) * (32 * V * NV) + lane * V;
+  const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
+  const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
+  unsigned m = __ballot_sync(0xffffffffu, row >= 0);
+  if (m == 0u) return;
+  const E* src = static_cast<const E*>(a.tok) + t * a.ldt;
+  Piece<E, V> p[NV];
 #pragma unroll
-            for (int j = 0; j < V; ++j) o.e[j] = float_to_elem<E>(wk * elem_to_float<E>(v.e[j]));
-          }
-          store_piece<E, V>(static_cast<E*>(a.rows_out) + r * a.ldro + c, o);
-        }
-        if (DOT) {
-          if (CODES) {
-            const int8_t* q = static_cast<const int8_t*>(a.rows_in) + r * a.ldr + c;
-            const float sc = scale_value(__ldg(a.scales + r * nb + (c >> 5)));  // V divides 32
+  for (int v = 0; v < NV; ++v) {
+    const int c = c0 + v * 32 * V;
+    p[v].zero();
+    if (c < a.d) p[v].load(src + c);
+  }
+  for (; m; m &= m - 1u) {
+    const int k = __ffs(m) - 1;
+    const float wk = __shfl_sync(0xffffffffu, w, k);
+    E* dst = static_cast<E*>(a.rows_out) + (long long)__shfl_sync(0xffffffffu, row, k) * a.ldro;
 #pragma unroll
-            for (int j = 0; j < V; ++j) dot = fmaf(elem_to_float<E>(v.e[j]), (float)q[j] * sc, dot);
-          } else {
-            const Piece<E, V> u = load_piece<E, V>(static_cast<const E*>(a.rows_in) + r * a.ldr + c);
+    for (int v = 0; v < NV; ++v) {
+      const int c = c0 + v * 32 * V;
+      if (c >= a.d) continue;
+      Piece<E, V> o = p[v];
+      if (a.w) {
+        float f[V];
+        p[v].get(f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) dot = fmaf(elem_to_float<E>(v.e[j]), elem_to_float<E>(u.e[j]), dot);
-          }
-        }
+        for (int j = 0; j < V; ++j) f[j] *= wk;
+        o.set(f);
       }
-      if (DOT) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == k) mydw = dot;
-      }
+      o.store(dst + c);
     }
-    if (DOT && lane < a.K) a.dw[t * a.K + lane] = mydw;
   }
 }
 
-static int row_grid(int T) {
-  const int wpb = kRowThreads / 32;
-  return (int)std::max<long long>(1, std::min<long long>(((long long)T + wpb - 1) / wpb, (long long)sm_count() * 8));
+// A piece of a row held in 8 bits, without its scale (V divides 32: one scale byte a piece).
+template <int V>
+struct CodePiece {
+  uint32_t word[V >= 4 ? V / 4 : 1];
+};
+template <int V>
+__device__ __forceinline__ CodePiece<V> load_codes(const int8_t* p) {
+  CodePiece<V> r;
+  if constexpr (V == 8) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    r.word[0] = v.x;
+    r.word[1] = v.y;
+  } else if constexpr (V == 4) {
+    r.word[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else {
+    static_assert(V == 1, "8, 4 or 1 codes");
+    r.word[0] = (uint8_t)__ldg(p);
+  }
+  return r;
+}
+
+// rows_out[slot_row[t,k]] = w[t,k] tok[t] (rows_out null: not written) and dw[t,k] = <tok[t],
+// rows_in[slot_row[t,k]]>, 0 for a slot without a row. WPT warps share a token, each every
+// WPT-th chunk of its columns; a dot product is summed in fp32 per lane, over the lanes by a
+// fixed shuffle tree and over the warps in order, so it does not depend on timing.
+template <typename E, int V, int NV, bool CODES>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowArgs a, int wpt) {
+  pdl_wait_then_release();
+  __shared__ float part[kRowWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % wpt;
+  const long long t = (long long)blockIdx.x * (kRowWarps / wpt) + warp / wpt;
+  const int nb = (a.d + 31) / 32;
+  float mydw = 0.f;
+  if (t < a.T) {
+    const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
+    const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
+    const E* src = static_cast<const E*>(a.tok) + t * a.ldt;
+    unsigned m = __ballot_sync(0xffffffffu, row >= 0);
+    while (m) {
+      const unsigned these = m;
+      int r[4];
+      float wk[4], dot[4] = {0.f, 0.f, 0.f, 0.f};
+      next_slots(m, row, w, r, wk);
+      for (int c0 = sub * 32 * V * NV + lane * V; c0 - lane * V < a.d; c0 += wpt * 32 * V * NV) {
+        Piece<E, V> g[NV], p[4][NV];
+        CodePiece<V> q[4][NV];
+        uint32_t sb[4][NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = c0 + v * 32 * V;
+          g[v].zero();
+          if (c < a.d) g[v].load(src + c);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (r[u] < 0) continue;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int c = c0 + v * 32 * V;
+            const long long at = (long long)r[u] * a.ldr + c;
+            if constexpr (CODES) {
+              sb[u][v] = 0;
+              if (c < a.d) {
+                q[u][v] = load_codes<V>(static_cast<const int8_t*>(a.rows_in) + at);
+                sb[u][v] = __ldg(a.scales + (long long)r[u] * nb + (c >> 5));
+              }
+            } else {
+              p[u][v].zero();
+              if (c < a.d) p[u][v].load(static_cast<const E*>(a.rows_in) + at);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (r[u] < 0) continue;
+          E* dst = static_cast<E*>(a.rows_out) + (long long)r[u] * a.ldro;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int c = c0 + v * 32 * V;
+            if (c >= a.d) continue;
+            float gf[V];
+            g[v].get(gf);
+            if constexpr (CODES) {
+              float s = 0.f;  // the sum over a piece, then its scale: a power of two, exact
+#pragma unroll
+              for (int j = 0; j < V; j += 4) {
+                float f[4];
+                codes_to_float(q[u][v].word[j / 4], f);
+#pragma unroll
+                for (int i = 0; i < (V < 4 ? V : 4); ++i) s = fmaf(gf[j + i], f[i], s);
+              }
+              dot[u] = fmaf(s, scale_value(sb[u][v]), dot[u]);
+            } else {
+              float pf[V];
+              p[u][v].get(pf);
+#pragma unroll
+              for (int j = 0; j < V; ++j) dot[u] = fmaf(gf[j], pf[j], dot[u]);
+            }
+            if (a.rows_out) {
+              Piece<E, V> o;
+#pragma unroll
+              for (int j = 0; j < V; ++j) gf[j] *= wk[u];
+              o.set(gf);
+              o.store(dst + c);
+            }
+          }
+        }
+      }
+      unsigned left = these;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float s = dot[u];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (left && lane == __ffs(left) - 1) mydw = s;
+        left &= left - 1u;
+      }
+    }
+  }
+  if (wpt > 1) {
+    part[warp][lane] = mydw;
+    __syncthreads();
+    if (sub == 0)
+      for (int i = 1; i < wpt; ++i) mydw += part[warp + i][lane];
+  }
+  if (sub == 0 && t < a.T && lane < a.K) a.dw[t * a.K + lane] = mydw;
+}
+
+// Chunks per token and the grid over them; false when the index space is too large for any
+// buffer of this GPU's memory.
+static bool row_items(RowArgs& a, int chunk) {
+  const int n = (int)(((long long)a.d + chunk - 1) / chunk);
+  if ((long long)a.T * n >= (long long)INT_MAX) return false;
+  a.chunks = FastDiv((uint32_t)n);
+  a.items = a.T * n;
+  return true;
+}
+
+template <typename E, int V, int NV>
+static int collect_go(RowArgs a, cudaStream_t st) {
+  if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
+  return launch_pdl(collect_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
 }
 
 template <typename E>
@@ -338,18 +515,36 @@ static int collect_run(const RowArgs& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(E);
   const bool vec = a.d % V == 0 && rows_aligned16(a.rows_in, a.ldr, sizeof(E)) &&
                    (!a.tok || rows_aligned16(a.tok, a.ldt, sizeof(E))) && rows_aligned16(a.tok_out, a.ldto, sizeof(E));
-  auto kern = vec ? collect_kernel<E, V> : collect_kernel<E, 1>;
-  return launch_pdl(kern, dim3(row_grid(a.T)), dim3(kRowThreads), 0, st, a);
+  return vec ? collect_go<E, V, kVecPieces>(a, st) : collect_go<E, 1, kElemPieces>(a, st);
 }
 
-template <typename E, bool DOT, bool CODES>
+template <typename E, int V, int NV>
+static int spread_go(RowArgs a, cudaStream_t st) {
+  if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
+  return launch_pdl(spread_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
+}
+
+template <typename E, int V, int NV, bool CODES>
+static int spread_dot_go(const RowArgs& a, cudaStream_t st) {
+  // more warps a token while the tokens alone do not fill the GPU and the row has chunks for them
+  int wpt = 1;
+  while (wpt < kRowWarps && (long long)a.T * wpt < (long long)sm_count() * 16 && a.d > wpt * 32 * V * NV) wpt *= 2;
+  const long long per_block = kRowWarps / wpt;
+  const dim3 grid((unsigned)((a.T + per_block - 1) / per_block));
+  return launch_pdl(spread_dot_kernel<E, V, NV, CODES>, grid, dim3(kRowThreads), 0, st, a, wpt);
+}
+
+template <typename E>
 static int spread_run(const RowArgs& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(E);
+  const bool codes = a.scales != nullptr;
   const bool vec = a.d % V == 0 && rows_aligned16(a.tok, a.ldt, sizeof(E)) &&
                    (!a.rows_out || rows_aligned16(a.rows_out, a.ldro, sizeof(E))) &&
-                   (!DOT || CODES || rows_aligned16(a.rows_in, a.ldr, sizeof(E)));
-  auto kern = vec ? spread_kernel<E, V, DOT, CODES> : spread_kernel<E, 1, DOT, CODES>;
-  return launch_pdl(kern, dim3(row_grid(a.T)), dim3(kRowThreads), 0, st, a);
+                   (!a.rows_in || (codes ? reinterpret_cast<uintptr_t>(a.rows_in) % V == 0
+                                         : rows_aligned16(a.rows_in, a.ldr, sizeof(E))));
+  if (!a.dw) return vec ? spread_go<E, V, kVecPieces>(a, st) : spread_go<E, 1, kElemPieces>(a, st);
+  if (codes) return vec ? spread_dot_go<E, V, kVecPieces, true>(a, st) : spread_dot_go<E, 1, kElemPieces, true>(a, st);
+  return vec ? spread_dot_go<E, V, kVecPieces, false>(a, st) : spread_dot_go<E, 1, kElemPieces, false>(a, st);
 }
 
 int launch_collect(int T, int K, long long rows, int d, int dtype, const void* rows_in, long long ldr, const float* w,
@@ -374,13 +569,6 @@ int launch_collect(int T, int K, long long rows, int d, int dtype, const void* r
                                   : collect_run<float>(a, st);
 }
 
-template <bool DOT, bool CODES>
-static int spread_types(int dtype, const RowArgs& a, cudaStream_t st) {
-  return dtype == MOE_DTYPE_BF16 ? spread_run<__nv_bfloat16, DOT, CODES>(a, st)
-         : dtype == MOE_DTYPE_F16 ? spread_run<__half, DOT, CODES>(a, st)
-                                  : spread_run<float, DOT, CODES>(a, st);
-}
-
 int launch_spread(int T, int K, long long rows, int d, int dtype, const void* tok, long long ldt, const void* rows_in,
                   long long ldr, const uint8_t* scales, const float* w, const int32_t* slot_row, void* rows_out,
                   long long ldro, float* dw, uint32_t* status, cudaStream_t st) {
@@ -400,8 +588,9 @@ int launch_spread(int T, int K, long long rows, int d, int dtype, const void* to
   a.T = T;
   a.K = K;
   a.d = d;
-  if (!dw) return spread_types<false, false>(dtype, a, st);
-  return scales ? spread_types<true, true>(dtype, a, st) : spread_types<true, false>(dtype, a, st);
+  return dtype == MOE_DTYPE_BF16 ? spread_run<__nv_bfloat16>(a, st)
+         : dtype == MOE_DTYPE_F16 ? spread_run<__half>(a, st)
+                                  : spread_run<float>(a, st);
 }
 
 }  // namespace moe
