@@ -14,24 +14,11 @@
 
 #include <algorithm>
 
-#ifndef KU
-#define KU 4
-#endif
-#ifndef KUS
-#define KUS 2
-#endif
-#ifndef KMB
-#define KMB 1
-#endif
-#ifndef KSB
-#define KSB 1
-#endif
-#ifndef KG
-#define KG 8
-#endif
 namespace moe {
 
 constexpr int kCkptThreads = 256;
+constexpr int kCkptCtas = 8;     // CTAs of the grid a multiprocessor
+constexpr int kSwigluCtas = 16;
 constexpr uint32_t kByteNan = 255u;
 
 // Scale byte of a block from its largest magnitude's fp32 bits.
@@ -42,15 +29,40 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
 // 2^-E (finite blocks: bytes 1 .. 248).
 __device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
 
-// rint(x 2^-E) clamped to +-127, as the low byte of 1.5 2^23 + code: the product is exact, so the
-// addition's rounding to nearest even is the only one (|x 2^-E| < 128).
+// rint(x 2^-E) as the low 16 bits of 1.5 2^23 + code: the product is exact, so the addition's
+// rounding to nearest even is the only one. |x 2^-E| < 128: the code is in [-128, 128] before the
+// clamp, which is taken on two 16-bit codes at a time.
 constexpr float kRoundBias = 12582912.f;
-__device__ __forceinline__ uint32_t quantise(float x, float inv) {
-  const float q = fmaf(x, inv, kRoundBias);
-  return __float_as_uint(fminf(fmaxf(q, kRoundBias - 127.f), kRoundBias + 127.f));
+__device__ __forceinline__ uint32_t quantise(float x, float inv) { return __float_as_uint(fmaf(x, inv, kRoundBias)); }
+__device__ __forceinline__ uint32_t clamp2(uint32_t two) {
+  return __vmaxs2(__vmins2(two, 0x007f007fu), 0xff81ff81u);
 }
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  return __byte_perm(clamp2(__byte_perm(a, b, 0x5410)), clamp2(__byte_perm(c, d, 0x5410)), 0x6420);
+}
+
+// Bits of the largest magnitude among the elements of a piece, as fp32 bits. The 16-bit types are
+// compared as bits, two at a time: magnitudes order as their bits do, infinity and NaN on top.
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_of(const Piece<E, V>& p) {
+  if constexpr (V == 4) {
+    return max(max(p.w.x & 0x7fffffffu, p.w.y & 0x7fffffffu), max(p.w.z & 0x7fffffffu, p.w.w & 0x7fffffffu));
+  } else {
+    return __vmaxu2(__vmaxu2(p.w.x & 0x7fff7fffu, p.w.y & 0x7fff7fffu),
+                    __vmaxu2(p.w.z & 0x7fff7fffu, p.w.w & 0x7fff7fffu));
+  }
+}
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_join(uint32_t a, uint32_t b) {
+  return V == 4 ? max(a, b) : __vmaxu2(a, b);
+}
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_bits(uint32_t t) {
+  if constexpr (V == 4) {
+    return t;
+  } else {
+    return __float_as_uint(word_to_float2<E>(max(t & 0xffffu, t >> 16)).x);
+  }
 }
 
 // Rows in use: *used clamped to [0, rows] (recorded when it lies outside), or all of them.
@@ -64,10 +76,10 @@ __device__ __forceinline__ long long rows_in_use(const int32_t* used, long long 
   return u;
 }
 
-// Eight consecutive elements as fp32, by 16-byte accesses.
-template <typename E>
-struct Eight {
-  static constexpr int V = 16 / sizeof(E), W = 8 / V;
+// N consecutive elements in 16-byte pieces.
+template <typename E, int N>
+struct Run {
+  static constexpr int V = 16 / sizeof(E), W = N / V;
   Piece<E, V> w[W];
   __device__ __forceinline__ void load(const E* p) {
 #pragma unroll
@@ -81,7 +93,7 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i].store(p + i * V);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(float (&v)[N]) const {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       float f[V];
@@ -90,13 +102,39 @@ struct Eight {
       for (int j = 0; j < V; ++j) v[i * V + j] = f[j];
     }
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
+  __device__ __forceinline__ void set(const float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       float f[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) f[j] = v[i * V + j];
       w[i].set(f);
+    }
+  }
+};
+
+// Work items (fixed pieces of a row) are taken in tiles of consecutive ones. A CTA starts at
+// tile blockIdx.x and goes on in steps of the whole grid; the row and the item in it follow by
+// addition, so that no 64-bit division is left in the loop.
+struct ItemPos {
+  long long row;
+  uint32_t i;
+};
+__device__ __forceinline__ ItemPos at(const ItemPos& s, uint32_t off, const FastDiv& per_row) {
+  const uint32_t n = s.i + off, q = per_row.quotient(n);
+  return {s.row + q, n - q * per_row.d};
+}
+struct Walk {
+  FastDiv per_row;    // items of a row
+  uint32_t tile;      // items of a tile
+  uint32_t step_rows, step_items;  // gridDim.x * tile items, as rows and items
+  __device__ __forceinline__ ItemPos begin() const { return at({0, 0u}, blockIdx.x * tile, per_row); }
+  __device__ __forceinline__ void next(ItemPos& s) const {
+    s.row += step_rows;
+    s.i += step_items;
+    if (s.i >= per_row.d) {
+      s.i -= per_row.d;
+      ++s.row;
     }
   }
 };
@@ -109,141 +147,198 @@ struct Ckpt8Args {
   const int32_t* used;
   uint32_t* status;
   long long rows, ld;
-  int cols, nb;     // nb: blocks (scale bytes) of a row
-  FastDiv per_row;  // work items of a row
+  int cols, nb;  // nb: blocks (scale bytes) of a row
+  Walk walk;
 };
 
-// Work items are cut into tiles of consecutive ones, a CTA's step. tile_start gives the row
-// and the item in it of a tile's first item; at() adds a thread's offset.
-struct ItemPos {
-  long long row;
-  uint32_t i;
+// Where an item of N columns lies. FLAT: dense rows of whole blocks, the tensor one long row, so
+// nothing is left to compute but the item's number; otherwise by its row.
+template <bool FLAT, int N>
+struct Spot {
+  long long x, code, scale;  // element offsets of its columns, its codes and its block's scale
+  uint32_t col;
+  __device__ __forceinline__ Spot(const Ckpt8Args& a, long long first, const ItemPos& s, uint32_t off) {
+    if constexpr (FLAT) {
+      x = code = (first + off) * N;
+      scale = (first + off) / (32 / N);
+      col = 0;
+    } else {
+      const ItemPos p = at(s, off, a.walk.per_row);
+      col = p.i * N;
+      x = p.row * a.ld + col;
+      code = p.row * a.cols + col;
+      scale = p.row * a.nb + p.i / (32 / N);
+    }
+  }
 };
-__device__ __forceinline__ ItemPos tile_start(long long first, const FastDiv& per_row) {
-  const long long row = first / per_row.d;
-  return {row, (uint32_t)(first - row * per_row.d)};
-}
-__device__ __forceinline__ ItemPos at(const ItemPos& s, uint32_t off, const FastDiv& per_row) {
-  const uint32_t n = s.i + off, q = per_row.quotient(n);
-  return {s.row + q, n - q * per_row.d};
-}
 
-// Store, rows of 16-byte pieces: an item is eight columns, four neighbouring lanes a block (a
-// row has 4 nb items; those past its end stand for zeros). kUnroll items a thread are loaded
-// before any is used.
-constexpr int kUnroll = KU;
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads, KMB) checkpoint8_kernel(Ckpt8Args a) {
+// Store, rows of 16-byte pieces: an item is half a block, two neighbouring lanes a block (a row
+// has 2 nb items; columns past its end stand for zeros). kUnroll items a thread are loaded before
+// any is used.
+constexpr int kItem = 16;
+constexpr int kUnroll = 4;
+template <typename E, bool FLAT>
+__global__ void __launch_bounds__(kCkptThreads, 2) checkpoint8_kernel(Ckpt8Args a) {
   pdl_wait_then_release();
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
-  constexpr int kTile = kCkptThreads * kUnroll;
-  for (long long first = (long long)blockIdx.x * kTile; first < n; first += (long long)gridDim.x * kTile) {
-    const ItemPos s = tile_start(first, a.per_row);
+  constexpr int kTile = kCkptThreads * kUnroll, V = 16 / sizeof(E), W = kItem / V;
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  ItemPos s = a.walk.begin();
+  for (long long first = (long long)blockIdx.x * kTile; first < n;
+       first += (long long)gridDim.x * kTile, a.walk.next(s)) {
     const uint32_t left = (uint32_t)min((long long)kTile, n - first);
-    Eight<E> x[kUnroll];
-    ItemPos p[kUnroll];
+    Run<E, kItem> x[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t off = u * kCkptThreads + threadIdx.x;
-      p[u] = at(s, off, a.per_row);
-      if (off < left && p[u].i * 8 < (uint32_t)a.cols)
-        x[u].load(static_cast<const E*>(a.x) + p[u].row * a.ld + p[u].i * 8);
-      else
-        x[u].zero();
+      const Spot<FLAT, kItem> p(a, first, s, off);
+      x[u].zero();
+      if (off < left) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (FLAT || p.col + i * V < (uint32_t)a.cols) x[u].w[i].load(static_cast<const E*>(a.x) + p.x + i * V);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      float v[8];
-      x[u].get(v);
-      uint32_t top = 0;
+      const uint32_t off = u * kCkptThreads + threadIdx.x;
+      const Spot<FLAT, kItem> p(a, first, s, off);
+      uint32_t top = top_of<E, V>(x[u].w[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t byte = scale_byte(top);
+      for (int i = 1; i < W; ++i) top = top_join<E, V>(top, top_of<E, V>(x[u].w[i]));
+      top = top_join<E, V>(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const uint32_t byte = scale_byte(top_bits<E, V>(top));
       const float inv = scale_inverse(byte);
-      uint2 q = make_uint2(pack4(quantise(v[0], inv), quantise(v[1], inv), quantise(v[2], inv), quantise(v[3], inv)),
-                           pack4(quantise(v[4], inv), quantise(v[5], inv), quantise(v[6], inv), quantise(v[7], inv)));
-      if (byte == kByteNan) q = make_uint2(0u, 0u);
-      if (u * kCkptThreads + threadIdx.x < left) {
-        if (p[u].i * 8 < (uint32_t)a.cols)
-          *reinterpret_cast<uint2*>(a.codes + p[u].row * a.cols + p[u].i * 8) = q;
-        if ((p[u].i & 3u) == 0u) a.scales[p[u].row * a.nb + (p[u].i >> 2)] = (uint8_t)byte;
+      float v[kItem];
+      x[u].get(v);
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q[j] = pack4(quantise(v[4 * j], inv), quantise(v[4 * j + 1], inv), quantise(v[4 * j + 2], inv),
+                     quantise(v[4 * j + 3], inv));
+        if (byte == kByteNan) q[j] = 0u;
+      }
+      if (off < left) {
+        if (FLAT) {
+          *reinterpret_cast<uint4*>(a.codes + p.code) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+          if (p.col < (uint32_t)a.cols) *reinterpret_cast<uint2*>(a.codes + p.code) = make_uint2(q[0], q[1]);
+          if (p.col + 8 < (uint32_t)a.cols) *reinterpret_cast<uint2*>(a.codes + p.code + 8) = make_uint2(q[2], q[3]);
+        }
+        if ((threadIdx.x & 1u) == 0u) a.scales[p.scale] = (uint8_t)byte;
       }
     }
   }
 }
 
 // Rows of any width and alignment: a warp takes kElemBlocks consecutive blocks of one row (an
-// item), a lane one element of each, so that all addresses are one base plus constants.
+// item), a lane one element of each, so that all addresses are one base plus constants. What is
+// the same for a whole block (its scale) is computed by one lane and handed round: the kernel is
+// bound by integer instructions (37 a block before that, at 77% of the ALU pipe: 93 us for
+// 60000 x 1001 in bf16).
 constexpr int kElemBlocks = 8;
 constexpr int kElemCols = 32 * kElemBlocks;
 constexpr int kCkptWarps = kCkptThreads / 32;
+
+// One item; FULL: all its columns are in the row.
+template <typename E, bool FULL>
+__device__ __forceinline__ void store_item(const E* x, int8_t* codes, uint8_t* scales, int left, int blocks) {
+  const int lane = threadIdx.x & 31;
+  float v[kElemBlocks];
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) v[u] = FULL || 32 * u < left ? elem_to_float<E>(__ldg(x + 32 * u)) : 0.f;
+  uint32_t top = 0;  // lane u: of block u
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) {
+    const uint32_t t = __reduce_max_sync(0xffffffffu, __float_as_uint(v[u]) & 0x7fffffffu);
+    if (lane == u) top = t;
+  }
+  const uint32_t byte = scale_byte(top);
+  const float inv = scale_inverse(byte);
+  const unsigned bad = __ballot_sync(0xffffffffu, byte == kByteNan);
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) {
+    const uint32_t q = clamp2(quantise(v[u], __shfl_sync(0xffffffffu, inv, u)));
+    if (FULL || 32 * u < left) codes[32 * u] = (int8_t)(((bad >> u) & 1u) ? 0u : q);
+  }
+  if (lane < blocks) scales[lane] = (uint8_t)byte;
+}
+
 template <typename E>
 __global__ void __launch_bounds__(kCkptThreads) checkpoint8_elem_kernel(Ckpt8Args a) {
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
-  for (long long first = (long long)blockIdx.x * kCkptWarps; first < n; first += (long long)gridDim.x * kCkptWarps) {
-    if (first + (threadIdx.x >> 5) >= n) break;  // warp-uniform
-    const ItemPos p = at(tile_start(first, a.per_row), threadIdx.x >> 5, a.per_row);
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  ItemPos p = at(a.walk.begin(), threadIdx.x >> 5, a.walk.per_row);  // this warp's item
+  for (long long i = (long long)blockIdx.x * kCkptWarps + (threadIdx.x >> 5); i < n;
+       i += (long long)gridDim.x * kCkptWarps, a.walk.next(p)) {
     const int c0 = (int)p.i * kElemCols;
     const int left = a.cols - c0 - lane;  // this lane's element of block u is in the row if 32 u < left
     const E* x = static_cast<const E*>(a.x) + p.row * a.ld + c0 + lane;
     int8_t* codes = a.codes + p.row * a.cols + c0 + lane;
-    float v[kElemBlocks];
-#pragma unroll
-    for (int u = 0; u < kElemBlocks; ++u) v[u] = 32 * u < left ? elem_to_float<E>(__ldg(x + 32 * u)) : 0.f;
-    uint32_t mine = 0;  // lane u: the scale byte of block u
-#pragma unroll
-    for (int u = 0; u < kElemBlocks; ++u) {
-      const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v[u]) & 0x7fffffffu));
-      const uint32_t q = quantise(v[u], scale_inverse(byte));
-      if (32 * u < left) codes[32 * u] = byte == kByteNan ? 0 : (int8_t)q;
-      if (lane == u) mine = byte;
-    }
-    const int blk = (int)p.i * kElemBlocks + lane;
-    if (lane < kElemBlocks && blk < a.nb) a.scales[p.row * a.nb + blk] = (uint8_t)mine;
+    uint8_t* scales = a.scales + p.row * a.nb + p.i * kElemBlocks;
+    const int blocks = min(kElemBlocks, a.nb - (int)p.i * kElemBlocks);
+    if (a.cols - c0 >= kElemCols)
+      store_item<E, true>(x, codes, scales, left, blocks);
+    else
+      store_item<E, false>(x, codes, scales, left, blocks);
   }
 }
 
-// Restore, rows of 16-byte pieces: an item is eight columns.
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads, KMB) restore8_kernel(Ckpt8Args a) {
+// Restore, rows of 16-byte pieces: an item is one of them, so that a warp's stores are whole
+// sectors (half a block a lane, as in the store, leaves 16 of every 32 bytes to a second
+// instruction: 28.8 against 27.3 us for 32768 x 1536 in bf16).
+constexpr int kRestoreUnroll = 8;
+template <typename E, bool FLAT>
+__global__ void __launch_bounds__(kCkptThreads) restore8_kernel(Ckpt8Args a) {
   pdl_wait_then_release();
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
-  constexpr int kTile = kCkptThreads * kUnroll;
-  for (long long first = (long long)blockIdx.x * kTile; first < n; first += (long long)gridDim.x * kTile) {
-    const ItemPos s = tile_start(first, a.per_row);
+  constexpr int V = 16 / sizeof(E), kTile = kCkptThreads * kRestoreUnroll;
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  ItemPos s = a.walk.begin();
+  for (long long first = (long long)blockIdx.x * kTile; first < n;
+       first += (long long)gridDim.x * kTile, a.walk.next(s)) {
     const uint32_t left = (uint32_t)min((long long)kTile, n - first);
-    uint2 q[kUnroll];
-    uint32_t byte[kUnroll];
-    ItemPos p[kUnroll];
+    CodePiece<V> q[kRestoreUnroll];
+    uint32_t byte[kRestoreUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kRestoreUnroll; ++u) {
       const uint32_t off = u * kCkptThreads + threadIdx.x;
-      p[u] = at(s, off, a.per_row);
-      if (off < left) {
-        q[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + p[u].row * a.cols + p[u].i * 8));
-        byte[u] = __ldg(a.scales + p[u].row * a.nb + (p[u].i >> 2));
-      }
+      if (off >= left) continue;
+      const Spot<FLAT, V> p(a, first, s, off);
+      q[u] = load_codes<V>(a.codes + p.code);
+      byte[u] = __ldg(a.scales + p.scale);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (u * kCkptThreads + threadIdx.x >= left) continue;
-      float lo[4], hi[4], v[8];
-      codes_to_float(q[u].x, lo);
-      codes_to_float(q[u].y, hi);
+    for (int u = 0; u < kRestoreUnroll; ++u) {
+      const uint32_t off = u * kCkptThreads + threadIdx.x;
+      if (off >= left) continue;
+      const Spot<FLAT, V> p(a, first, s, off);
       const float sc = scale_value(byte[u]);
+      float v[V];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = lo[j] * sc;
-        v[4 + j] = hi[j] * sc;
+      for (int j = 0; j < V / 4; ++j) {
+        float f[4];
+        codes_to_float(q[u].word[j], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * j + i] = f[i] * sc;
       }
-      Eight<E> o;
+      Piece<E, V> o;
       o.set(v);
-      o.store(static_cast<E*>(a.out) + p[u].row * a.ld + p[u].i * 8);
+      o.store(static_cast<E*>(a.out) + p.x);
     }
+  }
+}
+
+template <typename E, bool FULL>
+__device__ __forceinline__ void restore_item(const int8_t* codes, const uint8_t* scales, E* x, int left, int blocks) {
+  const int lane = threadIdx.x & 31;
+  int q[kElemBlocks];
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) q[u] = FULL || 32 * u < left ? (int)__ldg(codes + 32 * u) : 0;
+  const float sc = scale_value(lane < blocks ? (uint32_t)__ldg(scales + lane) : 0u);
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) {
+    const float v = (float)q[u] * __shfl_sync(0xffffffffu, sc, u);
+    if (FULL || 32 * u < left) x[32 * u] = float_to_elem<E>(v);
   }
 }
 
@@ -251,25 +346,20 @@ template <typename E>
 __global__ void __launch_bounds__(kCkptThreads) restore8_elem_kernel(Ckpt8Args a) {
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31;
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
-  for (long long first = (long long)blockIdx.x * kCkptWarps; first < n; first += (long long)gridDim.x * kCkptWarps) {
-    if (first + (threadIdx.x >> 5) >= n) break;
-    const ItemPos p = at(tile_start(first, a.per_row), threadIdx.x >> 5, a.per_row);
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  ItemPos p = at(a.walk.begin(), threadIdx.x >> 5, a.walk.per_row);
+  for (long long i = (long long)blockIdx.x * kCkptWarps + (threadIdx.x >> 5); i < n;
+       i += (long long)gridDim.x * kCkptWarps, a.walk.next(p)) {
     const int c0 = (int)p.i * kElemCols;
     const int left = a.cols - c0 - lane;
     E* x = static_cast<E*>(a.out) + p.row * a.ld + c0 + lane;
     const int8_t* codes = a.codes + p.row * a.cols + c0 + lane;
     const uint8_t* scales = a.scales + p.row * a.nb + p.i * kElemBlocks;
-    int q[kElemBlocks];
-    uint32_t byte[kElemBlocks];
-#pragma unroll
-    for (int u = 0; u < kElemBlocks; ++u) {
-      q[u] = 32 * u < left ? (int)__ldg(codes + 32 * u) : 0;
-      byte[u] = 32 * u < left ? (uint32_t)__ldg(scales + u) : 0u;
-    }
-#pragma unroll
-    for (int u = 0; u < kElemBlocks; ++u)
-      if (32 * u < left) x[32 * u] = float_to_elem<E>((float)q[u] * scale_value(byte[u]));
+    const int blocks = min(kElemBlocks, a.nb - (int)p.i * kElemBlocks);
+    if (a.cols - c0 >= kElemCols)
+      restore_item<E, true>(codes, scales, x, left, blocks);
+    else
+      restore_item<E, false>(codes, scales, x, left, blocks);
   }
 }
 
@@ -283,57 +373,82 @@ struct Swiglu8Args {
   uint32_t* status;
   long long rows, ldh, lddz, ldo;  // row strides of dh, dz and h
   int F, nb, packed;
-  FastDiv per_row;
+  Walk walk;
 };
 
 // da = dh b s (1 + a (1 - s)), db = dh a s, h = a s b with s = 1 / (1 + exp(-a)); fp32, one
-// rounding per output. expf and the fast division are within 2 ulp each; the division gives 0
+// rounding per output. expf is within 2 ulp and the approximate reciprocal within 1; it gives 0
 // where exp(-a) passes 2^126, as s is below fp32's normal range there.
 struct SwigluOut {
   float da, db, h;
 };
 __device__ __forceinline__ SwigluOut swiglu_grad(float a, float b, float g) {
-  const float s = __fdividef(1.f, 1.f + expf(-a));
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + expf(-a)));
   const float as = a * s;
   return {g * b * s * (1.f + a * (1.f - s)), g * as, as * b};
 }
 
-// Rows of 16-byte pieces: an item is eight pairs of pre-activations.
-constexpr int kSwigluUnroll = KUS;
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads, KSB) swiglu_backward8_kernel(Swiglu8Args a) {
+// Rows of 16-byte pieces: an item is eight pairs. FLAT: dense rows in the packed order, where the
+// pair's number over the whole tensor gives all offsets; otherwise by its row.
+constexpr int kSwigluUnroll = 2;
+constexpr int kPairs = 8;
+template <bool FLAT>
+struct PairSpot {
+  long long a, b, sa, sb, dh, da, db, h;  // offsets of its codes, scales, dh, dz and h
+  __device__ __forceinline__ PairSpot(const Swiglu8Args& g, long long first, const ItemPos& s, uint32_t off) {
+    if constexpr (FLAT) {
+      dh = h = (first + off) * kPairs;
+      a = da = 2 * dh - (dh & 63);  // (dh / 64) * 128 + dh % 64
+      b = db = a + 64;
+      sa = a >> 5;
+      sb = sa + 2;
+    } else {
+      const ItemPos p = at(s, off, g.walk.per_row);
+      const int f = (int)p.i * kPairs;
+      const int ca = g.packed ? (f >> 6) * 128 + (f & 63) : f, cb = g.packed ? ca + 64 : f + g.F;
+      const long long q = p.row * 2 * g.F, sc = p.row * g.nb, z = p.row * g.lddz;
+      a = q + ca;
+      b = q + cb;
+      sa = sc + (ca >> 5);
+      sb = sc + (cb >> 5);
+      dh = p.row * g.ldh + f;
+      h = p.row * g.ldo + f;
+      da = z + ca;
+      db = z + cb;
+    }
+  }
+};
+template <typename E, bool FLAT>
+__global__ void __launch_bounds__(kCkptThreads, 3) swiglu_backward8_kernel(Swiglu8Args a) {
   pdl_wait_then_release();
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
   constexpr int kTile = kCkptThreads * kSwigluUnroll;
-  for (long long first = (long long)blockIdx.x * kTile; first < n; first += (long long)gridDim.x * kTile) {
-    const ItemPos s = tile_start(first, a.per_row);
+  ItemPos s = a.walk.begin();
+  for (long long first = (long long)blockIdx.x * kTile; first < n;
+       first += (long long)gridDim.x * kTile, a.walk.next(s)) {
     const uint32_t left = (uint32_t)min((long long)kTile, n - first);
     uint2 qa[kSwigluUnroll], qb[kSwigluUnroll];
     uint32_t ba[kSwigluUnroll], bb[kSwigluUnroll];
-    Eight<E> g[kSwigluUnroll];
-    ItemPos p[kSwigluUnroll];
-    int ca[kSwigluUnroll], cb[kSwigluUnroll];
+    Run<E, kPairs> g[kSwigluUnroll];
 #pragma unroll
     for (int u = 0; u < kSwigluUnroll; ++u) {
       const uint32_t off = u * kCkptThreads + threadIdx.x;
-      p[u] = at(s, off, a.per_row);
-      const int f = (int)p[u].i * 8;
-      ca[u] = a.packed ? (f >> 6) * 128 + (f & 63) : f;
-      cb[u] = a.packed ? ca[u] + 64 : f + a.F;
+      const PairSpot<FLAT> p(a, first, s, off);
       if (off < left) {
-        const int8_t* q = a.codes + p[u].row * 2 * a.F;
-        const uint8_t* sc = a.scales + p[u].row * a.nb;
-        qa[u] = __ldg(reinterpret_cast<const uint2*>(q + ca[u]));
-        qb[u] = __ldg(reinterpret_cast<const uint2*>(q + cb[u]));
-        ba[u] = __ldg(sc + (ca[u] >> 5));
-        bb[u] = __ldg(sc + (cb[u] >> 5));
-        g[u].load(static_cast<const E*>(a.dh) + p[u].row * a.ldh + f);
+        qa[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + p.a));
+        qb[u] = __ldg(reinterpret_cast<const uint2*>(a.codes + p.b));
+        ba[u] = __ldg(a.scales + p.sa);
+        bb[u] = __ldg(a.scales + p.sb);
+        g[u].load(static_cast<const E*>(a.dh) + p.dh);
       }
     }
 #pragma unroll
     for (int u = 0; u < kSwigluUnroll; ++u) {
-      if (u * kCkptThreads + threadIdx.x >= left) continue;
-      float va[2][4], vb[2][4], gv[8], da[8], db[8], hv[8];
+      const uint32_t off = u * kCkptThreads + threadIdx.x;
+      if (off >= left) continue;
+      const PairSpot<FLAT> p(a, first, s, off);
+      float va[2][4], vb[2][4], gv[kPairs], da[kPairs], db[kPairs], hv[kPairs];
       codes_to_float(qa[u].x, va[0]);
       codes_to_float(qa[u].y, va[1]);
       codes_to_float(qb[u].x, vb[0]);
@@ -341,73 +456,101 @@ __global__ void __launch_bounds__(kCkptThreads, KSB) swiglu_backward8_kernel(Swi
       g[u].get(gv);
       const float sa = scale_value(ba[u]), sb = scale_value(bb[u]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kPairs; ++j) {
         const SwigluOut o = swiglu_grad(va[j / 4][j % 4] * sa, vb[j / 4][j % 4] * sb, gv[j]);
         da[j] = o.da;
         db[j] = o.db;
         hv[j] = o.h;
       }
-      Eight<E> o;
-      E* dz = static_cast<E*>(a.dz) + p[u].row * a.lddz;
+      Run<E, kPairs> o;
       o.set(da);
-      o.store(dz + ca[u]);
+      o.store(static_cast<E*>(a.dz) + p.da);
       o.set(db);
-      o.store(dz + cb[u]);
+      o.store(static_cast<E*>(a.dz) + p.db);
       if (a.h) {
         o.set(hv);
-        o.store(static_cast<E*>(a.h) + p[u].row * a.ldo + p[u].i * 8);
+        o.store(static_cast<E*>(a.h) + p.h);
       }
     }
   }
 }
 
-// Rows of any width and alignment: a warp takes 32 kElemPairs consecutive pairs of one row.
+// Rows of any width and alignment: a warp takes 32 kElemPairs consecutive pairs of one row, a lane
+// every 32nd. Lane u (and kElemPairs + u, ...) holds the scales that the u-th group of 32 pairs needs.
+// In the packed order a group's gate and up columns are each within one block; in halves the gate
+// columns are, and the up columns, F further on, may spread over two.
 constexpr int kElemPairs = 4;
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads) swiglu_backward8_elem_kernel(Swiglu8Args a) {
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.per_row.d;
-  for (long long first = (long long)blockIdx.x * kCkptWarps; first < n; first += (long long)gridDim.x * kCkptWarps) {
-    if (first + (threadIdx.x >> 5) >= n) break;
-    const ItemPos p = at(tile_start(first, a.per_row), threadIdx.x >> 5, a.per_row);
-    const int f0 = (int)p.i * 32 * kElemPairs + lane;
-    const int left = a.F - f0;
-    const int8_t* codes = a.codes + p.row * 2 * a.F;
-    const uint8_t* scales = a.scales + p.row * a.nb;
-    const E* dh = static_cast<const E*>(a.dh) + p.row * a.ldh + f0;
-    E* dz = static_cast<E*>(a.dz) + p.row * a.lddz;
-    int qa[kElemPairs], qb[kElemPairs];
-    uint32_t ba[kElemPairs], bb[kElemPairs];
-    float g[kElemPairs];
+template <typename E, bool PACKED, bool FULL>
+__device__ __forceinline__ void swiglu_item(const Swiglu8Args& g, long long row, int f0, int left) {
+  const int lane = threadIdx.x & 31, f = f0 + lane;
+  const int8_t* codes = g.codes + row * 2 * g.F;
+  const uint8_t* scales = g.scales + row * g.nb;
+  const E* dh = static_cast<const E*>(g.dh) + row * g.ldh + f;
+  // columns of the u-th pair: f0 is a multiple of 128, so in the packed order it is 2 f0 + ...
+  auto col_a = [&](int u) { return PACKED ? 2 * f0 + (u >> 1) * 128 + (u & 1) * 32 + lane : f + 32 * u; };
+  auto col_b = [&](int u) { return PACKED ? col_a(u) + 64 : f + 32 * u + g.F; };
+  int qa[kElemPairs], qb[kElemPairs];
+  float gv[kElemPairs];
 #pragma unroll
-    for (int u = 0; u < kElemPairs; ++u) {
-      if (32 * u >= left) continue;
-      const int f = f0 + 32 * u;
-      const int ca = a.packed ? (f >> 6) * 128 + (f & 63) : f, cb = a.packed ? ca + 64 : f + a.F;
-      qa[u] = __ldg(codes + ca);
-      qb[u] = __ldg(codes + cb);
-      ba[u] = __ldg(scales + (ca >> 5));
-      bb[u] = __ldg(scales + (cb >> 5));
-      g[u] = elem_to_float<E>(__ldg(dh + 32 * u));
-    }
+  for (int u = 0; u < kElemPairs; ++u) {
+    const bool ok = FULL || 32 * u < left;
+    qa[u] = ok ? (int)__ldg(codes + col_a(u)) : 0;
+    qb[u] = ok ? (int)__ldg(codes + col_b(u)) : 0;
+    gv[u] = ok ? elem_to_float<E>(__ldg(dh + 32 * u)) : 0.f;
+  }
+  // lanes 0 .. kElemPairs-1: the gate blocks; from lane 16: the up blocks in order
+  const int first_a = PACKED ? 2 * f0 / 32 : f0 / 32, first_b = PACKED ? first_a + 2 : (f0 + g.F) / 32;
+  const int l = lane & 15;
+  const int blk = PACKED ? (lane < 16 ? first_a : first_b) + (l >> 1) * 4 + (l & 1) : (lane < 16 ? first_a : first_b) + l;
+  const float sc = (l <= kElemPairs && blk < g.nb) ? scale_value(__ldg(scales + blk)) : 0.f;
+  const int over = PACKED ? 0 : (((f0 + g.F) & 31) + lane) >> 5;  // 1: the lane's up columns lie in the next block
+  E* dz = static_cast<E*>(g.dz) + row * g.lddz;
+  E* h = g.h ? static_cast<E*>(g.h) + row * g.ldo + f : nullptr;
 #pragma unroll
-    for (int u = 0; u < kElemPairs; ++u) {
-      if (32 * u >= left) continue;
-      const int f = f0 + 32 * u;
-      const int ca = a.packed ? (f >> 6) * 128 + (f & 63) : f, cb = a.packed ? ca + 64 : f + a.F;
-      const SwigluOut o = swiglu_grad((float)qa[u] * scale_value(ba[u]), (float)qb[u] * scale_value(bb[u]), g[u]);
-      dz[ca] = float_to_elem<E>(o.da);
-      dz[cb] = float_to_elem<E>(o.db);
-      if (a.h) static_cast<E*>(a.h)[p.row * a.ldo + f] = float_to_elem<E>(o.h);
+  for (int u = 0; u < kElemPairs; ++u) {
+    const float sa = __shfl_sync(0xffffffffu, sc, u), sb = __shfl_sync(0xffffffffu, sc, 16 + u + over);
+    const SwigluOut o = swiglu_grad((float)qa[u] * sa, (float)qb[u] * sb, gv[u]);
+    if (FULL || 32 * u < left) {
+      dz[col_a(u)] = float_to_elem<E>(o.da);
+      dz[col_b(u)] = float_to_elem<E>(o.db);
+      if (h) h[32 * u] = float_to_elem<E>(o.h);
     }
   }
 }
 
-// CTAs for `items` in tiles: at most eight a multiprocessor, each looping over its tiles.
-static unsigned tile_grid(long long rows, long long per_row, int tile) {
+template <typename E>
+__global__ void __launch_bounds__(kCkptThreads) swiglu_backward8_elem_kernel(Swiglu8Args a) {
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31;
+  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  ItemPos p = at(a.walk.begin(), threadIdx.x >> 5, a.walk.per_row);
+  for (long long i = (long long)blockIdx.x * kCkptWarps + (threadIdx.x >> 5); i < n;
+       i += (long long)gridDim.x * kCkptWarps, a.walk.next(p)) {
+    const int f0 = (int)p.i * 32 * kElemPairs;
+    const int left = a.F - f0 - lane;
+    const bool full = a.F - f0 >= 32 * kElemPairs;
+    if (a.packed) {
+      if (full) swiglu_item<E, true, true>(a, p.row, f0, left);
+      else swiglu_item<E, true, false>(a, p.row, f0, left);
+    } else {
+      if (full) swiglu_item<E, false, true>(a, p.row, f0, left);
+      else swiglu_item<E, false, false>(a, p.row, f0, left);
+    }
+  }
+}
+
+// The walk over rows of per_row items in tiles, and its grid: at most `ctas` CTAs a
+// multiprocessor, each looping over its tiles.
+static Walk make_walk(long long rows, long long per_row, int tile, int ctas, unsigned* grid) {
   const long long tiles = (rows * per_row + tile - 1) / tile;
-  return (unsigned)std::max<long long>(1, std::min<long long>(tiles, (long long)sm_count() * KG));
+  *grid = (unsigned)std::max<long long>(1, std::min<long long>(tiles, (long long)sm_count() * ctas));
+  const long long step = (long long)*grid * tile;
+  Walk w;
+  w.per_row = FastDiv((uint32_t)per_row);
+  w.tile = (uint32_t)tile;
+  w.step_rows = (uint32_t)(step / per_row);
+  w.step_items = (uint32_t)(step % per_row);
+  return w;
 }
 
 static Ckpt8Args ckpt8_args(long long rows, int cols, const int32_t* used, uint32_t* status) {
@@ -420,34 +563,48 @@ static Ckpt8Args ckpt8_args(long long rows, int cols, const int32_t* used, uint3
   return a;
 }
 
+// Rows whose columns lie in 16-byte pieces and whose codes in 8-byte ones; `flat`: dense rows of
+// whole blocks besides, codes in 16-byte pieces.
+static bool ckpt8_vec(const Ckpt8Args& a, const void* x, int bytes, bool* flat) {
+  const uintptr_t codes = reinterpret_cast<uintptr_t>(a.codes);
+  *flat = a.ld == a.cols && a.cols % 32 == 0 && codes % 16 == 0;
+  return a.cols % 8 == 0 && rows_aligned16(x, a.ld, bytes) && codes % 8 == 0;
+}
+
 template <typename E>
 static int checkpoint8_run(Ckpt8Args a, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && rows_aligned16(a.x, a.ld, sizeof(E)) &&
-                   reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-  a.per_row = FastDiv((uint32_t)(vec ? 4 * a.nb : (a.cols + kElemCols - 1) / kElemCols));
-  const int tile = vec ? kCkptThreads * kUnroll : kCkptWarps;
-  return launch_pdl(vec ? checkpoint8_kernel<E> : checkpoint8_elem_kernel<E>, dim3(tile_grid(a.rows, a.per_row.d, tile)),
-                    dim3(kCkptThreads), 0, st, a);
+  bool flat;
+  const bool vec = ckpt8_vec(a, a.x, sizeof(E), &flat);
+  unsigned grid;
+  a.walk = make_walk(a.rows, vec ? 2 * a.nb : (a.cols + kElemCols - 1) / kElemCols,
+                     vec ? kCkptThreads * kUnroll : kCkptWarps, kCkptCtas, &grid);
+  auto kern = !vec ? checkpoint8_elem_kernel<E> : flat ? checkpoint8_kernel<E, true> : checkpoint8_kernel<E, false>;
+  return launch_pdl(kern, dim3(grid), dim3(kCkptThreads), 0, st, a);
 }
 
 template <typename E>
 static int restore8_run(Ckpt8Args a, cudaStream_t st) {
-  const bool vec = a.cols % 8 == 0 && rows_aligned16(a.out, a.ld, sizeof(E)) &&
-                   reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-  a.per_row = FastDiv((uint32_t)(vec ? a.cols / 8 : (a.cols + kElemCols - 1) / kElemCols));
-  const int tile = vec ? kCkptThreads * kUnroll : kCkptWarps;
-  return launch_pdl(vec ? restore8_kernel<E> : restore8_elem_kernel<E>, dim3(tile_grid(a.rows, a.per_row.d, tile)),
-                    dim3(kCkptThreads), 0, st, a);
+  bool flat;
+  const bool vec = ckpt8_vec(a, a.out, sizeof(E), &flat);
+  unsigned grid;
+  a.walk = make_walk(a.rows, vec ? a.cols * (int)sizeof(E) / 16 : (a.cols + kElemCols - 1) / kElemCols,
+                     vec ? kCkptThreads * kRestoreUnroll : kCkptWarps, kCkptCtas, &grid);
+  auto kern = !vec ? restore8_elem_kernel<E> : flat ? restore8_kernel<E, true> : restore8_kernel<E, false>;
+  return launch_pdl(kern, dim3(grid), dim3(kCkptThreads), 0, st, a);
 }
 
 template <typename E>
 static int swiglu_backward8_run(Swiglu8Args a, cudaStream_t st) {
   const bool vec = a.F % 8 == 0 && rows_aligned16(a.dh, a.ldh, sizeof(E)) && rows_aligned16(a.dz, a.lddz, sizeof(E)) &&
                    (!a.h || rows_aligned16(a.h, a.ldo, sizeof(E))) && reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-  a.per_row = FastDiv((uint32_t)(vec ? a.F / 8 : (a.F + 32 * kElemPairs - 1) / (32 * kElemPairs)));
-  const int tile = vec ? kCkptThreads * kSwigluUnroll : kCkptWarps;
-  return launch_pdl(vec ? swiglu_backward8_kernel<E> : swiglu_backward8_elem_kernel<E>,
-                    dim3(tile_grid(a.rows, a.per_row.d, tile)), dim3(kCkptThreads), 0, st, a);
+  const bool flat = a.packed && a.ldh == a.F && a.lddz == 2 * a.F && (!a.h || a.ldo == a.F);
+  unsigned grid;
+  a.walk = make_walk(a.rows, vec ? a.F / kPairs : (a.F + 32 * kElemPairs - 1) / (32 * kElemPairs),
+                     vec ? kCkptThreads * kSwigluUnroll : kCkptWarps, kSwigluCtas, &grid);
+  auto kern = !vec ? swiglu_backward8_elem_kernel<E>
+              : flat ? swiglu_backward8_kernel<E, true>
+                     : swiglu_backward8_kernel<E, false>;
+  return launch_pdl(kern, dim3(grid), dim3(kCkptThreads), 0, st, a);
 }
 
 int launch_checkpoint8(long long rows, int cols, int dtype, const void* x, long long ldx, const int32_t* used,

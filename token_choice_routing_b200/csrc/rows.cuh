@@ -137,6 +137,27 @@ __device__ __forceinline__ void codes_to_float(uint32_t word, float (&v)[4]) {
   v[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7543)) - 8388736.f;
 }
 
+// A piece of a row held in 8 bits, without its scale (V divides 32: one scale byte a piece).
+template <int V>
+struct CodePiece {
+  uint32_t word[V >= 4 ? V / 4 : 1];
+};
+template <int V>
+__device__ __forceinline__ CodePiece<V> load_codes(const int8_t* p) {
+  CodePiece<V> r;
+  if constexpr (V == 8) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    r.word[0] = v.x;
+    r.word[1] = v.y;
+  } else if constexpr (V == 4) {
+    r.word[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  } else {
+    static_assert(V == 1, "8, 4 or 1 codes");
+    r.word[0] = (uint8_t)__ldg(p);
+  }
+  return r;
+}
+
 // 2^E of a scale byte, NaN for byte 255.
 __device__ __forceinline__ float scale_value(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);

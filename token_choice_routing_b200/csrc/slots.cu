@@ -365,27 +365,6 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(RowArgs a) {
   }
 }
 
-// A piece of a row held in 8 bits, without its scale (V divides 32: one scale byte a piece).
-template <int V>
-struct CodePiece {
-  uint32_t word[V >= 4 ? V / 4 : 1];
-};
-template <int V>
-__device__ __forceinline__ CodePiece<V> load_codes(const int8_t* p) {
-  CodePiece<V> r;
-  if constexpr (V == 8) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    r.word[0] = v.x;
-    r.word[1] = v.y;
-  } else if constexpr (V == 4) {
-    r.word[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else {
-    static_assert(V == 1, "8, 4 or 1 codes");
-    r.word[0] = (uint8_t)__ldg(p);
-  }
-  return r;
-}
-
 // rows_out[slot_row[t,k]] = w[t,k] tok[t] (rows_out null: not written) and dw[t,k] = <tok[t],
 // rows_in[slot_row[t,k]]>, 0 for a slot without a row. WPT warps share a token, each every
 // WPT-th chunk of its columns; a dot product is summed in fp32 per lane, over the lanes by a
