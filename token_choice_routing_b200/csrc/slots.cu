@@ -17,24 +17,35 @@ namespace moe {
 
 // ---------------------------------------------------------------------------------------
 // Sort. A counting sort over contiguous chunks of slots, one chunk per CTA: sort_count_kernel
-// writes each chunk's slots per expert, sort_place_kernel adds up the chunks below its own,
-// ranks its slots and writes their rows. Integer sums only, so the result is exact whatever
-// the order.
+// writes each chunk's slots per expert, sort_place_kernel ranks its chunk's slots, adds up the
+// chunks below its own and writes the rows. Integer sums only, so the result is exact whatever the
+// order. With one chunk the second kernel does it alone.
+//
+// What bounds it is the chain of dependent steps, not the 12 bytes a slot: the ids are read once
+// and stay in registers with their ranks, a slot's rank among the warp's earlier slots of its expert
+// comes from one match of the lanes and a running count in shared memory, and with two kernels the
+// ranking runs before the wait for the first one's table (the ids were complete before that kernel
+// let this one start).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortItems = 8;                              // slots a thread holds
+constexpr int kSortPass = kSortThreads * kSortItems;       // slots a CTA ranks at a time
 constexpr int kSortMaxChunks = 148;
-constexpr int kSortMinChunk = 4096;   // slots per CTA below which more CTAs are not worth it
+// One CTA does up to kSortOneChunk slots alone; more are cut into chunks of at least kSortMinChunk
+// (64 experts: 8192 slots 5.3 us, 6.2 with chunks of 2048 and 10.2 of 4096; alone, 4000 take 6.1 us).
+constexpr int kSortOneChunk = 2048;
+constexpr int kSortMinChunk = 1024;
 
 struct SortShape {
   long long S;
   int chunks;
-  long long per_chunk;  // a multiple of kSortThreads: every warp's share is a multiple of 32
+  long long per_chunk;  // a multiple of kSortThreads
 };
 
 static SortShape sort_shape(int T, int K) {
   SortShape s;
   s.S = (long long)T * K;
-  long long n = std::max<long long>(1, std::min<long long>(kSortMaxChunks, (s.S + kSortMinChunk - 1) / kSortMinChunk));
+  const long long n = std::max<long long>(1, s.S <= kSortOneChunk ? 1 : std::min<long long>(kSortMaxChunks, s.S / kSortMinChunk));
   s.per_chunk = std::max<long long>(1, ((s.S + n - 1) / n + kSortThreads - 1) / kSortThreads) * kSortThreads;
   s.chunks = (int)std::max<long long>(1, (s.S + s.per_chunk - 1) / s.per_chunk);
   return s;
@@ -53,7 +64,8 @@ struct SortArgs {
   uint32_t* status;
   int32_t* table;  // [chunks][N] slots per expert of each chunk
   long long S, per_chunk;
-  int K, N, chunks;
+  FastDiv K;
+  int N, chunks;
 };
 
 template <typename Id>
@@ -63,6 +75,20 @@ __device__ __forceinline__ int sort_id(const SortArgs& a, long long s, long long
   return (v >= 0 && v < (Id)a.N) ? (int)v : -1;
 }
 
+// The warp's lanes with the same id: one ballot per bit of the ids (a match instruction, one a
+// value, measured about three times the time of the whole ranking at 64 experts).
+template <int BITS>
+__device__ __forceinline__ unsigned same_id(int id) {
+  unsigned peers = __ballot_sync(0xffffffffu, id >= 0);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const bool bit = (id >> b) & 1;
+    const unsigned set = __ballot_sync(0xffffffffu, bit);
+    peers &= bit ? set : ~set;
+  }
+  return peers;
+}
+
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   pdl_wait_then_release();
@@ -70,119 +96,150 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
   for (int g = threadIdx.x; g < a.N; g += kSortThreads) s_hist[g] = 0;
   __syncthreads();
   const long long begin = a.per_chunk * blockIdx.x, end = min(a.S, begin + a.per_chunk);
-  for (long long s = begin + threadIdx.x; s < end; s += kSortThreads) {
-    const int id = sort_id<Id>(a, s, end);
-    if (id >= 0) atomicAdd(&s_hist[id], 1);
+  for (long long s0 = begin + threadIdx.x; s0 < end; s0 += kSortPass) {
+    int id[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) id[i] = sort_id<Id>(a, s0 + i * kSortThreads, end);
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i)
+      if (id[i] >= 0) atomicAdd(&s_hist[id[i]], 1);
   }
   __syncthreads();
   for (int g = threadIdx.x; g < a.N; g += kSortThreads) a.table[(size_t)blockIdx.x * a.N + g] = s_hist[g];
 }
 
-// Shared memory: whist [warps][N] (a warp's slots per expert, then its first row per expert),
-// tot [N] and pre [N] (all chunks, and the chunks below this one), part [32].
-template <typename Id>
+// Shared memory: whist [warps][N + 1] (a warp's slots per expert so far, then the slots of the
+// warps before it; rows padded so that a column is free of bank conflicts), tot [N] (this pass's
+// slots), base [N] (the row of the next slot), pre [N] (slots in the chunks below), part [32].
+template <typename Id, int BITS>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
-  pdl_wait_then_release();
   extern __shared__ int s_mem[];
-  const int N = a.N, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int N = a.N, tid = threadIdx.x, lane = tid & 31, w = tid >> 5, ld = N + 1;
   int* whist = s_mem;
-  int* tot = whist + kSortWarps * N;
-  int* pre = tot + N;
+  int* tot = whist + kSortWarps * ld;
+  int* base = tot + N;
+  int* pre = base + N;
   int* part = pre + N;
-  for (int i = tid; i < kSortWarps * N + 2 * N; i += kSortThreads) s_mem[i] = 0;
-  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
-  __syncthreads();
-  const long long per_warp = a.per_chunk / kSortWarps;
-  const long long begin = a.per_chunk * blockIdx.x + per_warp * w;
-  const long long end = min(a.S, begin + per_warp);
-  int* mine = whist + w * N;
-  for (long long s = begin + lane; s < end; s += 32) {
-    const int id = sort_id<Id>(a, s, end);
-    if (id >= 0) atomicAdd(&mine[id], 1);
-  }
-  if (a.chunks > 1) {
-    // column sums of the table: consecutive threads take consecutive entries, so each thread's
-    // expert changes with its step; integer atomics make the sums exact in any order
-    for (int i = tid; i < a.chunks * N; i += kSortThreads) {
-      const int c = i / N, g = i - c * N;
-      const int v = __ldg(a.table + i);
-      if (v) {
-        atomicAdd(&tot[g], v);
-        if (c < (int)blockIdx.x) atomicAdd(&pre[g], v);
+  if (a.chunks == 1) pdl_wait_then_release();  // nothing ran before this call's first kernel
+  for (int i = tid; i < N; i += kSortThreads) base[i] = pre[i] = 0;
+  const long long begin = a.per_chunk * blockIdx.x, end = min(a.S, begin + a.per_chunk);
+  bool first_pass = true;
+  for (long long p0 = begin; first_pass || p0 < end; p0 += kSortPass) {
+    // this pass's slots, an equal number of 32-slot groups for each warp
+    const int items = (int)min((long long)kSortItems, (end - p0 + kSortThreads - 1) / kSortThreads);
+    const long long mine0 = p0 + (long long)w * 32 * items + lane;
+    int id[kSortItems], rank[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) id[i] = i < items ? sort_id<Id>(a, mine0 + i * 32, end) : -1;
+    for (int i = tid; i < kSortWarps * ld; i += kSortThreads) whist[i] = 0;
+    __syncthreads();
+    int* mine = whist + w * ld;
+    unsigned peers[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) peers[i] = i < items ? same_id<BITS>(id[i]) : 0u;
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      if (i >= items) break;
+      if (id[i] >= 0) rank[i] = mine[id[i]] + __popc(peers[i] & ((1u << lane) - 1u));
+      __syncwarp();
+      if (id[i] >= 0 && lane == 31 - __clz(peers[i])) mine[id[i]] += __popc(peers[i]);
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int e = w; e < N; e += kSortWarps) {  // lane l: warp l's slots of expert e
+      const int v = whist[lane * ld + e];
+      int scan = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += u;
       }
+      whist[lane * ld + e] = scan - v;
+      if (lane == 31) tot[e] = scan;
     }
-  }
-  __syncthreads();
-  // first row of each warp's slots per expert, relative to the chunk's first row of that expert
-  int total = 0;
-  if (tid < N) {
-    int run = 0;
-    for (int ww = 0; ww < kSortWarps; ++ww) {
-      const int v = whist[ww * N + tid];
-      whist[ww * N + tid] = run;
-      run += v;
-    }
-    total = a.chunks > 1 ? tot[tid] : run;
-  }
-  // exclusive scan of the totals over the experts (N <= kSortThreads)
-  int scan = total;
+    if (first_pass) {
+      if (a.chunks > 1) {
+        pdl_wait_then_release();  // the table is complete
+        // column sums: thread (row c, expert g) takes every (kSortThreads / width)-th row
+        const int width = max(32, 1 << (32 - __clz(N - 1)));
+        const int g = tid & (width - 1), rows = kSortThreads / width;
+        int all = 0, below = 0;
+        if (g < N) {
+#pragma unroll 8
+          for (int c = tid / width; c < a.chunks; c += rows) {
+            const int v = __ldcg(a.table + (size_t)c * N + g);  // not the read-only path: written while this kernel runs
+            all += v;
+            below += c < (int)blockIdx.x ? v : 0;
+          }
+          atomicAdd(&base[g], all);
+          atomicAdd(&pre[g], below);
+        }
+        __syncthreads();
+      } else {
+        __syncthreads();
+        if (tid < N) base[tid] = tot[tid];
+        __syncthreads();
+      }
+      // exclusive scan of the totals over the experts (N <= kSortThreads)
+      const int total = tid < N ? base[tid] : 0;
+      int scan = total;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) part[w] = scan;
-  __syncthreads();
-  if (w == 0) {
-    int v = part[lane];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+      }
+      if (lane == 31) part[w] = scan;
+      __syncthreads();
+      if (w == 0) {
+        int v = part[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        part[lane] = v;
+      }
+      __syncthreads();
+      const int first = scan - total + (w > 0 ? part[w - 1] : 0);  // offsets[tid]
+      if (tid < N) {
+        if (blockIdx.x == 0) {
+          a.counts[tid] = total;
+          a.offsets[tid] = first;
+          if (tid == N - 1) a.offsets[N] = first + total;
+          if (tid == 0) *a.status = 0;
+        }
+        base[tid] = first + pre[tid];
+      }
+      first_pass = false;
     }
-    part[lane] = v;
-  }
-  __syncthreads();
-  const int first = scan - total + (w > 0 ? part[w - 1] : 0);  // offsets[tid]
-  if (tid < N) {
-    if (blockIdx.x == 0) {
-      a.counts[tid] = total;
-      a.offsets[tid] = first;
-      if (tid == N - 1) a.offsets[N] = first + total;
-    }
-    const int base = first + pre[tid];
-    for (int ww = 0; ww < kSortWarps; ++ww) whist[ww * N + tid] += base;
-  }
-  __syncthreads();
-  for (long long s0 = begin; s0 < end; s0 += 32) {  // warp-uniform trip count
-    const long long s = s0 + lane;
-    const int id = sort_id<Id>(a, s, end);
-    const unsigned peers = __match_any_sync(0xffffffffu, id);
-    int row = -1;
-    if (id >= 0) row = mine[id] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (id >= 0 && lane == 31 - __clz(peers)) mine[id] += __popc(peers);
-    __syncwarp();
-    if (s < end) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const long long s = mine0 + i * 32;
+      if (i >= items || s >= end) break;
+      const int row = id[i] >= 0 ? base[id[i]] + mine[id[i]] + rank[i] : -1;
       a.slot_row[s] = row;
-      if (row >= 0) a.perm_tok[row] = (int)((unsigned)s / (unsigned)a.K);
+      if (row >= 0) a.perm_tok[row] = (int)a.K.quotient((uint32_t)s);
     }
+    __syncthreads();
+    if (tid < N) base[tid] += tot[tid];
+    // the next pass clears whist only after its ids are loaded and syncs before it counts
   }
 }
 
 template <typename Id>
 static int sort_run(const SortArgs& a, cudaStream_t st) {
   const size_t count_smem = sizeof(int) * (size_t)a.N;
-  const size_t place_smem = sizeof(int) * ((size_t)(kSortWarps + 2) * a.N + 32);
+  const size_t place_smem = sizeof(int) * ((size_t)kSortWarps * (a.N + 1) + 3 * (size_t)a.N + 32);
+  auto place = a.N <= 64 ? sort_place_kernel<Id, 6> : sort_place_kernel<Id, 10>;
   if (place_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(sort_place_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_smem) !=
-          cudaSuccess)
+      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (a.chunks > 1) {
     const int r = launch_pdl(sort_count_kernel<Id>, dim3(a.chunks), dim3(kSortThreads), count_smem, st, a);
     if (r != MOE_OK) return r;
   }
-  return launch_pdl(sort_place_kernel<Id>, dim3(a.chunks), dim3(kSortThreads), place_smem, st, a);
+  return launch_pdl(place, dim3(a.chunks), dim3(kSortThreads), place_smem, st, a);
 }
 
 int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_t* counts, int32_t* offsets,
@@ -198,7 +255,7 @@ int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_
   a.table = ws_ptr<int32_t>(ws, 256);
   a.S = sh.S;
   a.per_chunk = sh.per_chunk;
-  a.K = K;
+  a.K = FastDiv((uint32_t)K);
   a.N = N;
   a.chunks = sh.chunks;
   return id_bytes == 8 ? sort_run<long long>(a, st) : sort_run<int>(a, st);
@@ -262,26 +319,17 @@ __device__ __forceinline__ void next_slots(unsigned& m, int row, float w, int (&
   }
 }
 
-// tok_out[t] = tok[t] + sum_k w[t,k] rows_in[slot_row[t,k]], fp32 sums in slot order.
-template <typename E, int V, int NV>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs a) {
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (item >= (uint32_t)a.items) return;
-  const long long t = a.chunks.quotient(item);
-  const int c0 = (int)(item - (uint32_t)t * a.chunks.d) * (32 * V * NV) + lane * V;
-  const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
-  const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
-  const E* base = static_cast<const E*>(a.tok) + t * a.ldt;
-  const E* rows_in = static_cast<const E*>(a.rows_in);
+// tok_out[t] = tok[t] + sum_k w[t,k] rows_in[slot_row[t,k]], fp32 sums in slot order. FULL: all
+// columns of the chunk are in the row.
+template <typename E, int V, int NV, bool FULL>
+__device__ __forceinline__ void collect_chunk(const RowArgs& a, long long t, int c0, int row, float w) {
+  const E* base = static_cast<const E*>(a.tok) + t * a.ldt + c0;
   float acc[NV][V];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = c0 + v * 32 * V;
     Piece<E, V> b;
     b.zero();
-    if (a.tok && c < a.d) b.load_own(base + c);
+    if (a.tok && (FULL || c0 + v * 32 * V < a.d)) b.load_own(base + v * 32 * V);
     b.get(acc[v]);
   }
   unsigned m = __ballot_sync(0xffffffffu, row >= 0);
@@ -292,12 +340,12 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs 
     Piece<E, V> p[4][NV];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const E* src = rows_in + (long long)r[u] * a.ldr;
+      const E* src = static_cast<const E*>(a.rows_in) + (long long)r[u] * a.ldr;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = c0 + v * 32 * V;
         p[u][v].zero();
-        if (r[u] >= 0 && c < a.d) p[u][v].load(src + c);
+        if (r[u] >= 0 && (FULL || c < a.d)) p[u][v].load(src + c);
       }
     }
 #pragma unroll
@@ -312,15 +360,32 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs 
       }
     }
   }
-  E* out = static_cast<E*>(a.tok_out) + t * a.ldto;
+  E* out = static_cast<E*>(a.tok_out) + t * a.ldto + c0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = c0 + v * 32 * V;
-    if (c >= a.d) continue;
+    if (!FULL && c0 + v * 32 * V >= a.d) continue;
     Piece<E, V> o;
     o.set(acc[v]);
-    o.store(out + c);
+    o.store(out + v * 32 * V);
   }
+}
+
+template <typename E, int V, int NV>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs a) {
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (item >= (uint32_t)a.items) return;
+  const long long t = a.chunks.quotient(item);
+  const int c0 = (int)(item - (uint32_t)t * a.chunks.d) * (32 * V * NV);
+  const int row = slot_row_checked(a.slot_row, t, lane, a.K, a.rows, a.status);
+  const float w = (a.w && lane < a.K) ? __ldg(a.w + t * a.K + lane) : 1.f;
+  // whole chunks apart only for single elements, where the kernel is bound by instructions
+  // (T = 16384, d = 1537, K = 8, bf16: 97 -> 86 us); with 16-byte pieces both paths together spill
+  if (V == 1 && c0 + 32 * V * NV <= a.d)
+    collect_chunk<E, V, NV, true>(a, t, c0 + lane * V, row, w);
+  else
+    collect_chunk<E, V, NV, false>(a, t, c0 + lane * V, row, w);
 }
 
 // rows_out[slot_row[t,k]] = w[t,k] tok[t] (w null: a copy).
@@ -365,12 +430,29 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(RowArgs a) {
   }
 }
 
+// The dot product of a piece with unscaled codes.
+template <int V>
+__device__ __forceinline__ float dot_codes(const float (&g)[V], const CodePiece<V>& q) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    float f[4];
+    codes_to_float(q.word[j / 4], f);
+#pragma unroll
+    for (int i = 0; i < (V < 4 ? V : 4); ++i) s = fmaf(g[j + i], f[i], s);
+  }
+  return s;
+}
+
 // rows_out[slot_row[t,k]] = w[t,k] tok[t] (rows_out null: not written) and dw[t,k] = <tok[t],
 // rows_in[slot_row[t,k]]>, 0 for a slot without a row. WPT warps share a token, each every
-// WPT-th chunk of its columns; a dot product is summed in fp32 per lane, over the lanes by a
+// WPT-th chunk of its columns; eight single elements of five rows a lane need more registers than
+// four CTAs leave (T = 16384, d = 1001, K = 4, bf16: 58 us with three CTAs, 94 with four; from codes
+// 79 us with two, 89 with three, 231 with four). A dot product is summed in fp32 per lane, over the lanes by a
 // fixed shuffle tree and over the warps in order, so it does not depend on timing.
 template <typename E, int V, int NV, bool CODES>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowArgs a, int wpt) {
+__global__ void __launch_bounds__(kRowThreads, V == 1 && NV == kElemPieces ? (CODES ? 2 : 3) : kRowCtas)
+    spread_dot_kernel(RowArgs a, int wpt) {
   pdl_wait_then_release();
   __shared__ float part[kRowWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -391,7 +473,14 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowAr
       for (int c0 = sub * 32 * V * NV + lane * V; c0 - lane * V < a.d; c0 += wpt * 32 * V * NV) {
         Piece<E, V> g[NV], p[4][NV];
         CodePiece<V> q[4][NV];
-        uint32_t sb[4][NV];
+        uint32_t sb[V == 1 ? 1 : 4][NV];
+        float lane_scale = 0.f;
+        if constexpr (CODES && V == 1) {
+          // 32 single elements are one block: lane u NV + v fetches slot u's scale of block v
+          const int u = lane / NV, blk = (c0 - lane) / 32 + lane % NV;
+          const int ru = u == 0 ? r[0] : u == 1 ? r[1] : u == 2 ? r[2] : r[3];
+          if (u < 4 && ru >= 0 && blk < nb) lane_scale = scale_value(__ldg(a.scales + (long long)ru * nb + blk));
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int c = c0 + v * 32 * V;
@@ -405,7 +494,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowAr
           for (int v = 0; v < NV; ++v) {
             const int c = c0 + v * 32 * V;
             const long long at = (long long)r[u] * a.ldr + c;
-            if constexpr (CODES) {
+            if constexpr (CODES && V == 1) {
+              q[u][v].word[0] = c < a.d ? (uint32_t)(int)__ldg(static_cast<const int8_t*>(a.rows_in) + at) : 0u;
+            } else if constexpr (CODES) {
               sb[u][v] = 0;
               if (c < a.d) {
                 q[u][v] = load_codes<V>(static_cast<const int8_t*>(a.rows_in) + at);
@@ -424,19 +515,15 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowAr
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             const int c = c0 + v * 32 * V;
-            if (c >= a.d) continue;
             float gf[V];
             g[v].get(gf);
-            if constexpr (CODES) {
-              float s = 0.f;  // the sum over a piece, then its scale: a power of two, exact
-#pragma unroll
-              for (int j = 0; j < V; j += 4) {
-                float f[4];
-                codes_to_float(q[u][v].word[j / 4], f);
-#pragma unroll
-                for (int i = 0; i < (V < 4 ? V : 4); ++i) s = fmaf(gf[j + i], f[i], s);
-              }
-              dot[u] = fmaf(s, scale_value(sb[u][v]), dot[u]);
+            if constexpr (CODES && V == 1)  // before any lane leaves; columns past the row hold zeros
+              dot[u] = fmaf(gf[0] * (float)(int)q[u][v].word[0], __shfl_sync(0xffffffffu, lane_scale, u * NV + v), dot[u]);
+            if (c >= a.d) continue;
+            if constexpr (CODES && V == 1) {
+            } else if constexpr (CODES) {
+              // the sum over a piece, then its scale: a power of two, exact
+              dot[u] = fmaf(dot_codes<V>(gf, q[u][v]), scale_value(sb[u][v]), dot[u]);
             } else {
               float pf[V];
               p[u][v].get(pf);
@@ -473,6 +560,126 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) spread_dot_kernel(RowAr
   if (sub == 0 && t < a.T && lane < a.K) a.dw[t * a.K + lane] = mydw;
 }
 
+// Narrow rows, of fewer pieces than a warp has lanes: a thread takes one piece of one token and
+// reads the token's slots itself, four at a time. (chunks: pieces of a row.)
+__device__ __forceinline__ void thread_slots(const RowArgs& a, long long t, int k0, int (&r)[4], float (&wk)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    r[u] = slot_row_checked(a.slot_row, t, k0 + u, a.K, a.rows, a.status);
+    wk[u] = (a.w && k0 + u < a.K) ? __ldg(a.w + t * a.K + k0 + u) : 1.f;
+  }
+}
+
+template <typename E, int V>
+__global__ void __launch_bounds__(kRowThreads) collect_narrow_kernel(RowArgs a) {
+  pdl_wait_then_release();
+  const uint32_t item = blockIdx.x * kRowThreads + threadIdx.x;
+  if (item >= (uint32_t)a.items) return;
+  const long long t = a.chunks.quotient(item);
+  const int c = (int)(item - (uint32_t)t * a.chunks.d) * V;
+  Piece<E, V> b;
+  b.zero();
+  if (a.tok) b.load_own(static_cast<const E*>(a.tok) + t * a.ldt + c);
+  float acc[V];
+  b.get(acc);
+  for (int k0 = 0; k0 < a.K; k0 += 4) {
+    int r[4];
+    float wk[4];
+    thread_slots(a, t, k0, r, wk);
+    Piece<E, V> p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      p[u].zero();
+      if (r[u] >= 0) p[u].load(static_cast<const E*>(a.rows_in) + (long long)r[u] * a.ldr + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (r[u] < 0) continue;
+      float f[V];
+      p[u].get(f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = fmaf(wk[u], f[j], acc[j]);
+    }
+  }
+  b.set(acc);
+  b.store(static_cast<E*>(a.tok_out) + t * a.ldto + c);
+}
+
+template <typename E, int V>
+__device__ __forceinline__ Piece<E, V> scaled(const Piece<E, V>& p, float w) {
+  float f[V];
+  p.get(f);
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] *= w;
+  Piece<E, V> o;
+  o.set(f);
+  return o;
+}
+
+template <typename E, int V>
+__global__ void __launch_bounds__(kRowThreads) spread_narrow_kernel(RowArgs a) {
+  pdl_wait_then_release();
+  const uint32_t item = blockIdx.x * kRowThreads + threadIdx.x;
+  if (item >= (uint32_t)a.items) return;
+  const long long t = a.chunks.quotient(item);
+  const int c = (int)(item - (uint32_t)t * a.chunks.d) * V;
+  Piece<E, V> p;
+  p.load(static_cast<const E*>(a.tok) + t * a.ldt + c);
+  for (int k0 = 0; k0 < a.K; k0 += 4) {
+    int r[4];
+    float wk[4];
+    thread_slots(a, t, k0, r, wk);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (r[u] >= 0)
+        (a.w ? scaled<E, V>(p, wk[u]) : p).store(static_cast<E*>(a.rows_out) + (long long)r[u] * a.ldro + c);
+  }
+}
+
+// A group of G lanes a token, a piece each.
+template <typename E, int V, bool CODES>
+__global__ void __launch_bounds__(kRowThreads) spread_dot_narrow_kernel(RowArgs a, int G) {
+  pdl_wait_then_release();
+  const int j = threadIdx.x & (G - 1), c = j * V;
+  const long long t = (long long)blockIdx.x * (kRowThreads / G) + threadIdx.x / G;
+  const bool token = t < a.T, mine = token && c < a.d;
+  const int nb = (a.d + 31) / 32;
+  Piece<E, V> g;
+  g.zero();
+  if (mine) g.load(static_cast<const E*>(a.tok) + t * a.ldt + c);
+  float gf[V];
+  g.get(gf);
+  for (int k0 = 0; k0 < a.K; k0 += 4) {  // uniform trip count: the shuffles below are the warp's
+    int r[4] = {-1, -1, -1, -1};
+    float wk[4], dot[4];
+    if (token) thread_slots(a, t, k0, r, wk);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      dot[u] = 0.f;
+      if (!mine || r[u] < 0) continue;
+      const long long at = (long long)r[u] * a.ldr + c;
+      if constexpr (CODES) {
+        const CodePiece<V> q = load_codes<V>(static_cast<const int8_t*>(a.rows_in) + at);
+        const float sc = scale_value(__ldg(a.scales + (long long)r[u] * nb + (c >> 5)));
+        dot[u] = dot_codes<V>(gf, q) * sc;
+      } else {
+        Piece<E, V> p;
+        p.load(static_cast<const E*>(a.rows_in) + at);
+        float f[V];
+        p.get(f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot[u] = fmaf(gf[i], f[i], dot[u]);
+      }
+      if (a.rows_out) scaled<E, V>(g, wk[u]).store(static_cast<E*>(a.rows_out) + (long long)r[u] * a.ldro + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      for (int o = G >> 1; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+      if (token && j == 0 && k0 + u < a.K) a.dw[t * a.K + k0 + u] = dot[u];
+    }
+  }
+}
+
 // Chunks per token and the grid over them; false when the index space is too large for any
 // buffer of this GPU's memory.
 static bool row_items(RowArgs& a, int chunk) {
@@ -483,8 +690,20 @@ static bool row_items(RowArgs& a, int chunk) {
   return true;
 }
 
+// Rows of at most this many pieces go to the narrow kernels, where a warp would leave half of its
+// lanes idle and do a token's slot lookup for little (T = 65536, K = 8, bf16, unpermute: d = 64
+// 53 -> 17 us, 256 60 -> 53 us; 512, beyond, 80 against 98 us). Single elements: d = 33 50 -> 27 us,
+// 127, beyond, 56 against 94 us.
+template <int V>
+constexpr int kNarrow = V == 1 ? 64 : 32 * V;
+
 template <typename E, int V, int NV>
 static int collect_go(RowArgs a, cudaStream_t st) {
+  if (a.d <= kNarrow<V>) {
+    if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
+    return launch_pdl(collect_narrow_kernel<E, V>, dim3((a.items + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0,
+                      st, a);
+  }
   if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
   return launch_pdl(collect_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
 }
@@ -494,17 +713,30 @@ static int collect_run(const RowArgs& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(E);
   const bool vec = a.d % V == 0 && rows_aligned16(a.rows_in, a.ldr, sizeof(E)) &&
                    (!a.tok || rows_aligned16(a.tok, a.ldt, sizeof(E))) && rows_aligned16(a.tok_out, a.ldto, sizeof(E));
-  return vec ? collect_go<E, V, kVecPieces>(a, st) : collect_go<E, 1, kElemPieces>(a, st);
+  if (vec) return collect_go<E, V, kVecPieces>(a, st);
+  return a.d <= 128 ? collect_go<E, 1, 4>(a, st) : collect_go<E, 1, kElemPieces>(a, st);
 }
 
 template <typename E, int V, int NV>
 static int spread_go(RowArgs a, cudaStream_t st) {
+  if (a.d <= kNarrow<V>) {
+    if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
+    return launch_pdl(spread_narrow_kernel<E, V>, dim3((a.items + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0,
+                      st, a);
+  }
   if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
   return launch_pdl(spread_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
 }
 
 template <typename E, int V, int NV, bool CODES>
 static int spread_dot_go(const RowArgs& a, cudaStream_t st) {
+  if (a.d <= 32 * V) {  // a lane a piece
+    int G = 1;
+    while (G * V < a.d) G *= 2;
+    const int per_block = kRowThreads / G;
+    return launch_pdl(spread_dot_narrow_kernel<E, V, CODES>, dim3((a.T + per_block - 1) / per_block), dim3(kRowThreads),
+                      0, st, a, G);
+  }
   // more warps a token while the tokens alone do not fill the GPU and the row has chunks for them
   int wpt = 1;
   while (wpt < kRowWarps && (long long)a.T * wpt < (long long)sm_count() * 16 && a.d > wpt * 32 * V * NV) wpt *= 2;
@@ -522,8 +754,11 @@ static int spread_run(const RowArgs& a, cudaStream_t st) {
                    (!a.rows_in || (codes ? reinterpret_cast<uintptr_t>(a.rows_in) % V == 0
                                          : rows_aligned16(a.rows_in, a.ldr, sizeof(E))));
   if (!a.dw) return vec ? spread_go<E, V, kVecPieces>(a, st) : spread_go<E, 1, kElemPieces>(a, st);
-  if (codes) return vec ? spread_dot_go<E, V, kVecPieces, true>(a, st) : spread_dot_go<E, 1, kElemPieces, true>(a, st);
-  return vec ? spread_dot_go<E, V, kVecPieces, false>(a, st) : spread_dot_go<E, 1, kElemPieces, false>(a, st);
+  if (vec)
+    return codes ? spread_dot_go<E, V, kVecPieces, true>(a, st) : spread_dot_go<E, V, kVecPieces, false>(a, st);
+  if (a.d <= 64) return codes ? spread_dot_go<E, 1, 2, true>(a, st) : spread_dot_go<E, 1, 2, false>(a, st);
+  if (a.d <= 128) return codes ? spread_dot_go<E, 1, 4, true>(a, st) : spread_dot_go<E, 1, 4, false>(a, st);
+  return codes ? spread_dot_go<E, 1, kElemPieces, true>(a, st) : spread_dot_go<E, 1, kElemPieces, false>(a, st);
 }
 
 int launch_collect(int T, int K, long long rows, int d, int dtype, const void* rows_in, long long ldr, const float* w,
