@@ -19,35 +19,40 @@ namespace moe {
 // Sort. A counting sort over contiguous chunks of slots, one chunk per CTA: sort_count_kernel
 // writes each chunk's slots per expert, sort_place_kernel ranks its chunk's slots, adds up the
 // chunks below its own and writes the rows. Integer sums only, so the result is exact whatever the
-// order. With one chunk the second kernel does it alone.
+// order. With one chunk the placing kernel does it alone.
 //
-// What bounds it is the chain of dependent steps, not the 12 bytes a slot: the ids are read once
-// and stay in registers with their ranks, a slot's rank among the warp's earlier slots of its expert
-// comes from one match of the lanes and a running count in shared memory, and with two kernels the
-// ranking runs before the wait for the first one's table (the ids were complete before that kernel
-// let this one start).
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 8;                              // slots a thread holds
-constexpr int kSortPass = kSortThreads * kSortItems;       // slots a CTA ranks at a time
+// What bounds it is instructions and the chain of dependent steps, not the 12 bytes a slot. So the
+// ids are read once and stay in registers with their ranks, and with two kernels the ranking runs
+// before the wait for the first one's table (the ids were complete before that kernel let this one
+// start): 1M slots, 64 experts 14.1 us, of which the ranking and the launch are 6.6 us; 256 slots 3.0 us.
+// Ranks written by a first kernel and only offset by a second one took 14.3 us, and 10.2 against 7.1
+// at 256k slots. A warp takes 32 slots at a time; lanes of the same id find each other by one ballot per
+// bit of the ids (a match instruction, which goes value by value, took 13 against 5 us for 16384
+// slots; counters of a byte per lane and expert, summed by multiplication, took the same time as
+// the ballots at 1M slots and more at fewer).
+constexpr int kSortItems = 8;  // slots a thread holds; a CTA ranks 256 a warp at a time
 constexpr int kSortMaxChunks = 148;
-// One CTA does up to kSortOneChunk slots alone; more are cut into chunks of at least kSortMinChunk
-// (64 experts: 8192 slots 5.3 us, 6.2 with chunks of 2048 and 10.2 of 4096; alone, 4000 take 6.1 us).
+// One CTA does up to kSortOneChunk slots alone; more are cut into chunks of 1024 slots, or more once
+// there are kSortMaxChunks of them (64 experts: 8192 slots 4.7 us; in chunks of 4096 10.2 us).
 constexpr int kSortOneChunk = 2048;
-constexpr int kSortMinChunk = 1024;
+// 16 warps a CTA while they rank a chunk in one pass, 32 beyond (a single step of 256 slots 3.0 us
+// against 3.7 with 32 warps; 1M slots, 512 experts 28.9 against 42.7 with 16).
+constexpr int kSortFewWarps = 4096;
 
 struct SortShape {
   long long S;
   int chunks;
-  long long per_chunk;  // a multiple of kSortThreads
+  long long per_chunk;  // a multiple of 1024
+  int warps;            // of a CTA: 16 or 32
 };
 
 static SortShape sort_shape(int T, int K) {
   SortShape s;
   s.S = (long long)T * K;
-  const long long n = std::max<long long>(1, s.S <= kSortOneChunk ? 1 : std::min<long long>(kSortMaxChunks, s.S / kSortMinChunk));
-  s.per_chunk = std::max<long long>(1, ((s.S + n - 1) / n + kSortThreads - 1) / kSortThreads) * kSortThreads;
+  const long long n = s.S <= kSortOneChunk ? 1 : std::min<long long>(kSortMaxChunks, (s.S + 1023) / 1024);
+  s.per_chunk = std::max<long long>(1, ((s.S + n - 1) / n + 1023) / 1024) * 1024;
   s.chunks = (int)std::max<long long>(1, (s.S + s.per_chunk - 1) / s.per_chunk);
+  s.warps = s.per_chunk <= kSortFewWarps ? 16 : 32;
   return s;
 }
 
@@ -68,6 +73,7 @@ struct SortArgs {
   int N, chunks;
 };
 
+// The slot's expert, -1 for none.
 template <typename Id>
 __device__ __forceinline__ int sort_id(const SortArgs& a, long long s, long long end) {
   if (s >= end) return -1;
@@ -75,8 +81,139 @@ __device__ __forceinline__ int sort_id(const SortArgs& a, long long s, long long
   return (v >= 0 && v < (Id)a.N) ? (int)v : -1;
 }
 
-// The warp's lanes with the same id: one ballot per bit of the ids (a match instruction, one a
-// value, measured about three times the time of the whole ranking at 64 experts).
+template <typename Id, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) sort_count_kernel(SortArgs a) {
+  constexpr int kThreads = WARPS * 32, kPass = kThreads * kSortItems;
+  pdl_wait_then_release();
+  extern __shared__ int s_mem[];
+  int* hist = s_mem;
+  for (int g = threadIdx.x; g < a.N; g += kThreads) hist[g] = 0;
+  __syncthreads();
+  const long long begin = a.per_chunk * blockIdx.x, end = min(a.S, begin + a.per_chunk);
+  for (long long s0 = begin + threadIdx.x; s0 < end; s0 += kPass) {
+    int id[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) id[i] = sort_id<Id>(a, s0 + i * kThreads, end);
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i)
+      if (id[i] >= 0) atomicAdd(&hist[id[i]], 1);
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < a.N; g += kThreads) a.table[(size_t)blockIdx.x * a.N + g] = hist[g];
+}
+
+// Shared memory of the placing kernel: whist [warps][N + 1] (a warp's slots per expert, then the
+// row of its first one; padded so that a column is free of bank conflicts), tot [N] (this pass's
+// slots), base [N] (the row of the next slot), pre [N] (slots in the chunks below), part [32].
+struct SortShared {
+  int *whist, *tot, *base, *pre, *part;
+  int ld;
+  __device__ __forceinline__ SortShared(int* mem, int N, int warps) {
+    ld = N + 1;
+    whist = mem;
+    tot = whist + warps * ld;
+    base = tot + N;
+    pre = base + N;
+    part = pre + N;
+  }
+};
+static size_t sort_smem(int N, int warps) { return sizeof(int) * ((size_t)warps * (N + 1) + 3 * (size_t)N + 32); }
+
+// First pass of a chunk: base [e] = the row of this chunk's first slot of expert e, from the table
+// (one chunk: from tot); CTA 0 writes counts and offsets. tot and whist are complete and synced.
+template <int WARPS>
+__device__ __forceinline__ void sort_first_rows(const SortArgs& a, const SortShared& m) {
+  constexpr int kThreads = WARPS * 32;
+  const int N = a.N, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (a.chunks > 1) {
+    // column sums: a thread takes expert g in every (kThreads / width)-th row. Not the
+    // read-only path: the table is written while this kernel runs.
+    const int width = min(kThreads, max(32, 1 << (32 - __clz(N - 1)))), rows = kThreads / width;
+    for (int g = tid & (width - 1); g < N; g += width) {
+      int all = 0, below = 0;
+#pragma unroll 8
+      for (int c = tid / width; c < a.chunks; c += rows) {
+        const int v = __ldcg(a.table + (size_t)c * N + g);
+        all += v;
+        below += c < (int)blockIdx.x ? v : 0;
+      }
+      atomicAdd(&m.base[g], all);
+      atomicAdd(&m.pre[g], below);
+    }
+  } else {
+    for (int e = tid; e < N; e += kThreads) m.base[e] = m.tot[e];
+  }
+  __syncthreads();
+  // exclusive scan of the totals over the experts, two a thread (N <= 1024 <= 2 threads)
+  const int e0 = 2 * tid, t0 = e0 < N ? m.base[e0] : 0, t1 = e0 + 1 < N ? m.base[e0 + 1] : 0;
+  int scan = t0 + t1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) m.part[w] = scan;
+  __syncthreads();
+  if (w == 0) {
+    int v = lane < WARPS ? m.part[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < WARPS; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    m.part[lane] = v;
+  }
+  __syncthreads();
+  const int first = scan - t0 - t1 + (w > 0 ? m.part[w - 1] : 0);  // offsets[e0]
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = e0 + j;
+    if (e >= N) continue;
+    const int at = first + j * t0;
+    if (blockIdx.x == 0) {
+      a.counts[e] = j ? t1 : t0;
+      a.offsets[e] = at;
+      if (e == N - 1) a.offsets[N] = first + t0 + t1;
+    }
+    m.base[e] = at + m.pre[e];
+  }
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
+  __syncthreads();
+}
+
+// whist: a warp's slots per expert -> the slots of the warps before it; tot: of all warps. WARPS
+// lanes take an expert, lane l of them the l-th warp's slots.
+template <int WARPS>
+__device__ __forceinline__ void sort_warp_scan(const SortShared& m, int N) {
+  constexpr int kPerWarp = 32 / WARPS;  // experts a warp takes at a time
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int e0 = kPerWarp * w; e0 < N; e0 += kPerWarp * WARPS) {
+    const int e = e0 + lane / WARPS, l = lane % WARPS;
+    const int v = e < N ? m.whist[l * m.ld + e] : 0;
+    int scan = v;
+#pragma unroll
+    for (int o = 1; o < WARPS; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, scan, o, WARPS);
+      if (l >= o) scan += u;
+    }
+    if (e < N) {
+      m.whist[l * m.ld + e] = scan - v;
+      if (l == WARPS - 1) m.tot[e] = scan;
+    }
+  }
+}
+
+// One pass's steps between a warp's ranks and the rows; returns with base + whist in place.
+template <int WARPS>
+__device__ __forceinline__ void sort_join(const SortArgs& a, const SortShared& m, bool first_pass) {
+  __syncthreads();
+  sort_warp_scan<WARPS>(m, a.N);
+  if (first_pass && a.chunks > 1) pdl_wait_then_release();  // the table is complete
+  __syncthreads();
+  if (first_pass) sort_first_rows<WARPS>(a, m);
+}
+
+// The warp's lanes with the same id, below 2^BITS.
 template <int BITS>
 __device__ __forceinline__ unsigned same_id(int id) {
   unsigned peers = __ballot_sync(0xffffffffu, id >= 0);
@@ -89,52 +226,27 @@ __device__ __forceinline__ unsigned same_id(int id) {
   return peers;
 }
 
-template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
-  pdl_wait_then_release();
-  extern __shared__ int s_hist[];
-  for (int g = threadIdx.x; g < a.N; g += kSortThreads) s_hist[g] = 0;
-  __syncthreads();
-  const long long begin = a.per_chunk * blockIdx.x, end = min(a.S, begin + a.per_chunk);
-  for (long long s0 = begin + threadIdx.x; s0 < end; s0 += kSortPass) {
-    int id[kSortItems];
-#pragma unroll
-    for (int i = 0; i < kSortItems; ++i) id[i] = sort_id<Id>(a, s0 + i * kSortThreads, end);
-#pragma unroll
-    for (int i = 0; i < kSortItems; ++i)
-      if (id[i] >= 0) atomicAdd(&s_hist[id[i]], 1);
-  }
-  __syncthreads();
-  for (int g = threadIdx.x; g < a.N; g += kSortThreads) a.table[(size_t)blockIdx.x * a.N + g] = s_hist[g];
-}
-
-// Shared memory: whist [warps][N + 1] (a warp's slots per expert so far, then the slots of the
-// warps before it; rows padded so that a column is free of bank conflicts), tot [N] (this pass's
-// slots), base [N] (the row of the next slot), pre [N] (slots in the chunks below), part [32].
-template <typename Id, int BITS>
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
+template <typename Id, int WARPS, int BITS>
+__global__ void __launch_bounds__(WARPS * 32) sort_place_kernel(SortArgs a) {
+  constexpr int kThreads = WARPS * 32, kPass = kThreads * kSortItems;
   extern __shared__ int s_mem[];
-  const int N = a.N, tid = threadIdx.x, lane = tid & 31, w = tid >> 5, ld = N + 1;
-  int* whist = s_mem;
-  int* tot = whist + kSortWarps * ld;
-  int* base = tot + N;
-  int* pre = base + N;
-  int* part = pre + N;
-  if (a.chunks == 1) pdl_wait_then_release();  // nothing ran before this call's first kernel
-  for (int i = tid; i < N; i += kSortThreads) base[i] = pre[i] = 0;
+  const SortShared m(s_mem, a.N, WARPS);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (a.chunks == 1) pdl_wait_then_release();  // this is the call's first kernel
+  for (int i = tid; i < a.N; i += kThreads) m.base[i] = m.pre[i] = 0;
   const long long begin = a.per_chunk * blockIdx.x, end = min(a.S, begin + a.per_chunk);
   bool first_pass = true;
-  for (long long p0 = begin; first_pass || p0 < end; p0 += kSortPass) {
-    // this pass's slots, an equal number of 32-slot groups for each warp
-    const int items = (int)min((long long)kSortItems, (end - p0 + kSortThreads - 1) / kSortThreads);
+  for (long long p0 = begin; first_pass || p0 < end; p0 += kPass) {
+    // an equal number of 32-slot groups for each warp
+    const int items = (int)min((long long)kSortItems, (end - p0 + kThreads - 1) / kThreads);
     const long long mine0 = p0 + (long long)w * 32 * items + lane;
     int id[kSortItems], rank[kSortItems];
+    unsigned peers[kSortItems];
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) id[i] = i < items ? sort_id<Id>(a, mine0 + i * 32, end) : -1;
-    for (int i = tid; i < kSortWarps * ld; i += kSortThreads) whist[i] = 0;
+    for (int i = tid; i < WARPS * m.ld; i += kThreads) m.whist[i] = 0;
     __syncthreads();
-    int* mine = whist + w * ld;
-    unsigned peers[kSortItems];
+    int* mine = m.whist + w * m.ld;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) peers[i] = i < items ? same_id<BITS>(id[i]) : 0u;
 #pragma unroll
@@ -145,101 +257,39 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
       if (id[i] >= 0 && lane == 31 - __clz(peers[i])) mine[id[i]] += __popc(peers[i]);
       __syncwarp();
     }
-    __syncthreads();
-    for (int e = w; e < N; e += kSortWarps) {  // lane l: warp l's slots of expert e
-      const int v = whist[lane * ld + e];
-      int scan = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += u;
-      }
-      whist[lane * ld + e] = scan - v;
-      if (lane == 31) tot[e] = scan;
-    }
-    if (first_pass) {
-      if (a.chunks > 1) {
-        pdl_wait_then_release();  // the table is complete
-        // column sums: thread (row c, expert g) takes every (kSortThreads / width)-th row
-        const int width = max(32, 1 << (32 - __clz(N - 1)));
-        const int g = tid & (width - 1), rows = kSortThreads / width;
-        int all = 0, below = 0;
-        if (g < N) {
-#pragma unroll 8
-          for (int c = tid / width; c < a.chunks; c += rows) {
-            const int v = __ldcg(a.table + (size_t)c * N + g);  // not the read-only path: written while this kernel runs
-            all += v;
-            below += c < (int)blockIdx.x ? v : 0;
-          }
-          atomicAdd(&base[g], all);
-          atomicAdd(&pre[g], below);
-        }
-        __syncthreads();
-      } else {
-        __syncthreads();
-        if (tid < N) base[tid] = tot[tid];
-        __syncthreads();
-      }
-      // exclusive scan of the totals over the experts (N <= kSortThreads)
-      const int total = tid < N ? base[tid] : 0;
-      int scan = total;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += v;
-      }
-      if (lane == 31) part[w] = scan;
-      __syncthreads();
-      if (w == 0) {
-        int v = part[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += u;
-        }
-        part[lane] = v;
-      }
-      __syncthreads();
-      const int first = scan - total + (w > 0 ? part[w - 1] : 0);  // offsets[tid]
-      if (tid < N) {
-        if (blockIdx.x == 0) {
-          a.counts[tid] = total;
-          a.offsets[tid] = first;
-          if (tid == N - 1) a.offsets[N] = first + total;
-          if (tid == 0) *a.status = 0;
-        }
-        base[tid] = first + pre[tid];
-      }
-      first_pass = false;
-    }
-    __syncthreads();
+    sort_join<WARPS>(a, m, first_pass);
+    first_pass = false;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
       const long long s = mine0 + i * 32;
       if (i >= items || s >= end) break;
-      const int row = id[i] >= 0 ? base[id[i]] + mine[id[i]] + rank[i] : -1;
+      const int row = id[i] >= 0 ? m.base[id[i]] + mine[id[i]] + rank[i] : -1;
       a.slot_row[s] = row;
       if (row >= 0) a.perm_tok[row] = (int)a.K.quotient((uint32_t)s);
     }
     __syncthreads();
-    if (tid < N) base[tid] += tot[tid];
-    // the next pass clears whist only after its ids are loaded and syncs before it counts
+    for (int e = tid; e < a.N; e += kThreads) m.base[e] += m.tot[e];
   }
 }
 
-template <typename Id>
-static int sort_run(const SortArgs& a, cudaStream_t st) {
-  const size_t count_smem = sizeof(int) * (size_t)a.N;
-  const size_t place_smem = sizeof(int) * ((size_t)kSortWarps * (a.N + 1) + 3 * (size_t)a.N + 32);
-  auto place = a.N <= 64 ? sort_place_kernel<Id, 6> : sort_place_kernel<Id, 10>;
-  if (place_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)place_smem) != cudaSuccess)
+template <typename Id, int WARPS>
+static int sort_go(const SortArgs& a, cudaStream_t st) {
+  auto place = a.N <= 64 ? sort_place_kernel<Id, WARPS, 6> : sort_place_kernel<Id, WARPS, 10>;
+  const size_t smem = sort_smem(a.N, WARPS);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
+  const dim3 grid(a.chunks), block(WARPS * 32);
   if (a.chunks > 1) {
-    const int r = launch_pdl(sort_count_kernel<Id>, dim3(a.chunks), dim3(kSortThreads), count_smem, st, a);
+    const int r = launch_pdl(sort_count_kernel<Id, WARPS>, grid, block, sizeof(int) * (size_t)a.N, st, a);
     if (r != MOE_OK) return r;
   }
-  return launch_pdl(place, dim3(a.chunks), dim3(kSortThreads), place_smem, st, a);
+  return launch_pdl(place, grid, block, smem, st, a);
+}
+
+template <typename Id>
+static int sort_run(const SortArgs& a, int warps, cudaStream_t st) {
+  return warps == 16 ? sort_go<Id, 16>(a, st) : sort_go<Id, 32>(a, st);
 }
 
 int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_t* counts, int32_t* offsets,
@@ -258,7 +308,7 @@ int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_
   a.K = FastDiv((uint32_t)K);
   a.N = N;
   a.chunks = sh.chunks;
-  return id_bytes == 8 ? sort_run<long long>(a, st) : sort_run<int>(a, st);
+  return id_bytes == 8 ? sort_run<long long>(a, sh.warps, st) : sort_run<int>(a, sh.warps, st);
 }
 
 // ---------------------------------------------------------------------------------------
