@@ -693,11 +693,32 @@ MOE_API int moe_swiglu_backward8(int64_t rows, int64_t F, int32_t packed, int32_
                                  void* dz, int64_t lddz, void* h, int64_t ldh, void* status,
                                  moe_stream_t stream);
 
+/* The 8-bit checkpoint of one forward (device pointers, written by moe_forward_checkpoint8): the
+ * gate/up pre-activations and the routed outputs. Codes on 16-byte, scales on 4-byte
+ * boundaries. */
+typedef struct moe_codes8 {
+  int8_t* z_codes;            /* [R_cap, 2F]  routed pre-activations, packed order    */
+  uint8_t* z_scales;          /* [R_cap, 2F / 32]                                     */
+  int8_t* zs_codes;           /* [T, 2F_shared]  the shared expert's                  */
+  uint8_t* zs_scales;         /* [T, 2F_shared / 32]                                  */
+  int8_t* ys_codes;           /* [R_cap, d]  routed outputs                           */
+  uint8_t* ys_scales;         /* [R_cap, d / 32]                                      */
+} moe_codes8_t;
+
+/* moe_forward that keeps the pre-activations and the routed outputs for
+ * moe_backward_checkpoint8: the codes and scales that moe_checkpoint8 gives for moe_forward's z,
+ * z_shared and ys (routed ones below offsets[N]; the rows behind are left as they were). The
+ * pre-activations are stored by the gate/up GEMM's epilogue and never go to memory in bf16:
+ * out->z and out->z_shared are not used. out->xs and out->logits must be set, out->shared_out
+ * may be NULL or y as in moe_forward. What out holds of xs, h, h_shared and ys is scratch
+ * afterwards. */
+MOE_API int moe_forward_checkpoint8(const moe_dims_t* dims, const moe_weights_t* w, const uint16_t* x,
+                                    const float* tok_null_bias, const moe_outputs_t* out,
+                                    const moe_codes8_t* codes, void* workspace, moe_stream_t stream);
+
 /* What moe_backward_checkpoint8 reads of a forward (device pointers): the fields of
- * moe_saved_t that are kept as they are, and in 8 bits the gate/up pre-activations z, z_shared
- * and the routed outputs ys (each moe_checkpoint8 of the forward's buffer; the routed ones
- * with rows_used = offsets + N). xs and h are not kept: the rows are gathered from x again and
- * h is recomputed. */
+ * moe_saved_t that are kept as they are, and the 8-bit blocks of moe_forward_checkpoint8. xs and h
+ * are not kept: the rows are gathered from x again and h is recomputed. */
 typedef struct moe_saved8 {
   const uint16_t* x;          /* [T, d] bf16 layer input                              */
   const float* logits;        /* [T, N+1+C+V]                                         */

@@ -281,7 +281,7 @@ def layer_step(cfg):
     inp = I.make_inputs(cfg)
     layer, x, tnb = H.make_layer(inp)
     dy = bf16_tensor(I.upstream_grad(cfg), "cuda")
-    out = layer.alloc(cfg.T, save_preact=True)
+    out = layer.alloc(cfg.T)
     ck = layer.alloc_checkpoint8(cfg.T)
     o = layer.forward_checkpoint8(x, tnb, out, ck)
     return layer, x, tnb, dy, out, ck, o
@@ -319,8 +319,8 @@ def test_training_step_from_an_8_bit_checkpoint(name):
         p = z.float().view(-1, F // 64, 2, 64)
         h.copy_((p[:, :, 0] * torch.sigmoid(p[:, :, 0]) * p[:, :, 1]).reshape(-1, F))
     want = layer.backward(x, near, dy, ALPHA, BETA)
-    out["z"].fill_(float("nan"))                       # scratch: another layer's forward has it now
-    out["ys"].fill_(float("nan"))
+    out["ys"].fill_(float("nan"))                      # scratch: another layer's forward has it now
+    out["h_shared"].fill_(float("nan"))
     out["xs"].fill_(float("nan"))
     out["h"].fill_(float("nan"))
     got = layer.backward_checkpoint8(x, ck, dy, ALPHA, BETA)
@@ -334,6 +334,30 @@ def test_training_step_from_an_8_bit_checkpoint(name):
         assert rel(g, w) <= 5e-3, (n, rel(g, w))
         assert rel(g, e) <= 3e-2, (n, rel(g, e))
     assert R >= 0
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+@pytest.mark.parametrize("combine", ["inplace", "fused"])
+def test_forward_checkpoint_is_bitwise_the_stored_forward(name, combine):
+    """The codes that the gate/up GEMM's epilogue writes are those of moe_checkpoint8 on the
+    pre-activations that the training forward writes in bf16."""
+    cfg = CASES[name]
+    inp = I.make_inputs(cfg)
+    layer, x, tnb = H.make_layer(inp)
+    want = layer.forward(x, tnb, layer.alloc(cfg.T, save_preact=True, combine=combine))
+    ck = layer.alloc_checkpoint8(cfg.T)
+    for n in B.SAVED8_CODES:
+        ck[n].fill_(99)
+    got = layer.forward_checkpoint8(x, tnb, layer.alloc(cfg.T, combine=combine), ck)
+    torch.cuda.synchronize()
+    assert B.get_device_status(got["workspace"]) == B.OK
+    for n in ("y", "logits", "topk_idx", "slot_row", "offsets", "losses"):
+        assert torch.equal(got[n], want[n]), n
+    R = int(want["offsets"][-1])
+    for name, key, used in (("z", "z", R), ("zs", "z_shared", cfg.T), ("ys", "ys", R)):
+        codes, scales = (torch.full_like(ck[f"{name}_{w}"], 99) for w in ("codes", "scales"))
+        B.checkpoint8(want[key][:used], codes[:used], scales[:used])
+        assert torch.equal(ck[name + "_codes"], codes) and torch.equal(ck[name + "_scales"], scales), name
 
 
 def test_checkpointed_layers_share_their_scratch():
@@ -388,9 +412,9 @@ def test_checkpoint_refusals():
     cfg = CASES["ragged"]
     layer, x, tnb, dy, out, ck, _ = layer_step(cfg)
     with pytest.raises(ValueError):
-        layer.forward_checkpoint8(x, tnb, layer.alloc(cfg.T), ck)
+        layer.forward_checkpoint8(x, tnb, layer.alloc(cfg.T, xs=False), ck)
     with pytest.raises(ValueError):
-        layer.forward_checkpoint8(x, tnb, layer.alloc(cfg.T - 1, save_preact=True), ck)
+        layer.forward_checkpoint8(x, tnb, layer.alloc(cfg.T - 1), ck)
     with pytest.raises(ValueError):
         layer.forward_checkpoint8(x, tnb, out, layer.alloc_checkpoint8(cfg.T - 1))
     with pytest.raises(ValueError):

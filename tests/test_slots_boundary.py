@@ -136,6 +136,28 @@ def test_backward_checkpoint8_refusals():
     assert call(dims=B.dims(0, 128, 8, 8, 4, 64, 64)) == B.OK
 
 
+def test_forward_checkpoint8_refusals():
+    dm = B.dims(256, 128, 8, 8, 4, 64, 64)
+    w = B.Weights(*[4096] * 8)
+
+    def call(out=None, code=None, value=None, dims=dm, ws=P):
+        o, q = B.Outputs(*[4096] * len(B.OUTPUT_FIELDS)), B.Codes8(*[4096] * 6)
+        if out:
+            setattr(o, out, value)
+        if code:
+            setattr(q, code, value)
+        return B.LIB.moe_forward_checkpoint8(C.byref(dims), C.byref(w), P, NUL, C.byref(o), C.byref(q), ws, NUL)
+
+    for n in ("xs", "logits", "topk_idx", "slot_row", "h", "ys", "y", "offsets", "losses"):
+        assert call(out=n) == INV, n
+    for n in B.SAVED8_CODES:
+        assert call(code=n) == INV, n
+        assert call(code=n, value=4096 + (8 if n.endswith("codes") else 2)) == INV, n   # alignment
+    assert call(ws=NUL) == INV
+    assert call(dims=B.dims(256, 100, 8, 8, 4, 64, 64)) == UNS
+    assert call(dims=B.dims(0, 128, 8, 8, 4, 64, 64)) == B.OK
+
+
 def test_saved8_layout_matches_the_header(tmp_path):
     import os
     import shutil
@@ -147,12 +169,15 @@ def test_saved8_layout_matches_the_header(tmp_path):
     fields = [f for f, _ in B.Saved8._fields_]
     src = ['#include <stdio.h>', '#include <stddef.h>', '#include "moe_null.h"', "int main(void) {"]
     src += [f'  printf("%zu\\n", offsetof(moe_saved8_t, {f}));' for f in fields]
-    src += ['  printf("%zu\\n", sizeof(moe_saved8_t));', "  return 0;", "}"]
+    src += ['  printf("%zu\\n", sizeof(moe_saved8_t));']
+    src += [f'  printf("%zu\\n", offsetof(moe_codes8_t, {f}));' for f, _ in B.Codes8._fields_]
+    src += ["  return 0;", "}"]
     (tmp_path / "l.c").write_text("\n".join(src) + "\n")
     exe = str(tmp_path / "l")
     subprocess.run([cc, "-I", os.path.join(root, "include"), str(tmp_path / "l.c"), "-o", exe], check=True)
     got = [int(v) for v in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()]
-    assert got == [getattr(B.Saved8, f).offset for f in fields] + [C.sizeof(B.Saved8)]
+    assert got == ([getattr(B.Saved8, f).offset for f in fields] + [C.sizeof(B.Saved8)] +
+                   [getattr(B.Codes8, f).offset for f, _ in B.Codes8._fields_])
 
 
 # ---------------------------------------------------------------------- the binding's checks

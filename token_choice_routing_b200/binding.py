@@ -62,6 +62,10 @@ SAVED8_FIELDS = ("x", "logits", "topk_idx", "topk_gate", "offsets", "slot_row", 
 SAVED8_CODES = ("z_codes", "z_scales", "zs_codes", "zs_scales", "ys_codes", "ys_scales")
 
 
+class Codes8(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in SAVED8_CODES]
+
+
 class Saved8(C.Structure):
     _fields_ = ([(n, C.c_void_p) for n in SAVED8_FIELDS] + [("t_total", C.c_int64)] +
                 [(n, C.c_void_p) for n in SAVED8_CODES])
@@ -135,6 +139,8 @@ def _load() -> C.CDLL:
         "moe_checkpoint8": (i32, [i64, i64, i32, vp, i64, vp, vp, vp, vp, vp]),
         "moe_restore8": (i32, [i64, i64, i32, vp, vp, vp, vp, i64, vp, vp]),
         "moe_swiglu_backward8": (i32, [i64, i64, i32, i32, vp, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp]),
+        "moe_forward_checkpoint8": (i32, [pd, C.POINTER(Weights), vp, vp, C.POINTER(Outputs), C.POINTER(Codes8), vp,
+                                          vp]),
         "moe_backward_checkpoint8_workspace_bytes": (sz, [pd]),
         "moe_backward_checkpoint8": (i32, [pd, C.POINTER(Weights), C.POINTER(Saved8), vp, C.c_float, C.c_float,
                                            C.POINTER(Grads), vp, vp]),
@@ -416,6 +422,13 @@ def expert_swiglu_backward_saved(dm, offsets, z, z_shared, bws, stream=None):
     _check("moe_expert_swiglu_backward_saved",
            LIB.moe_expert_swiglu_backward_saved(C.byref(dm), _p(offsets), _p(z), _p(z_shared), _p(bws),
                                                 _stream(stream)))
+
+
+def forward_checkpoint8(dm, weights: Weights, x, tok_null_bias, outputs: Outputs, codes: Codes8, ws, stream=None):
+    """moe_forward that keeps an 8-bit checkpoint for ``backward_checkpoint8``."""
+    _check("moe_forward_checkpoint8",
+           LIB.moe_forward_checkpoint8(C.byref(dm), C.byref(weights), _p(x), _p(tok_null_bias), C.byref(outputs),
+                                       C.byref(codes), _p(ws), _stream(stream)))
 
 
 def backward_checkpoint8_workspace_bytes(dm: Dims) -> int:

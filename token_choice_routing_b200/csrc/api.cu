@@ -54,6 +54,46 @@ using namespace moe;
 
 static inline cudaStream_t S(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+static int check_forward(const moe_dims_t* dims, const moe_weights_t* w, const uint16_t* x, const moe_outputs_t* out,
+                         const void* workspace) {
+  if (!w || !out || !x || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!w->w_router || !w->gate_up || !w->w_down || !w->shared_gate_up || !w->shared_down)
+    return MOE_ERR_INVALID_ARG;
+  if (dims->V > 0 && !w->const_vectors) return MOE_ERR_INVALID_ARG;
+  if (!out->topk_idx || !out->topk_gate || !out->n_real || !out->counts || !out->offsets || !out->perm_tok ||
+      !out->slot_row || !out->h || !out->h_shared || !out->ys || !out->y || !out->counts_ext || !out->P ||
+      !out->losses)
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// The whole forward; with q, the pre-activations go to its 8-bit blocks.
+static int forward_run(const moe_dims_t& d, const moe_weights_t* w, const uint16_t* x, const float* tok_null_bias,
+                       const moe_outputs_t* out, const moe_codes8_t* q, void* workspace, cudaStream_t st) {
+  MOE_CHECK(launch_route(d, x, w->w_router, w->router_bias, tok_null_bias, out->logits, out->topk_idx,
+                         out->topk_gate, out->n_real, workspace, st, w->router_split));
+  MOE_CHECK(launch_dispatch(d, x, out->topk_idx, workspace, out->counts, out->offsets, out->perm_tok,
+                            out->slot_row, out->xs, out->counts_ext, out->P, out->losses, st));
+  if (q || out->z) {
+    // training: the pre-activations are kept for the backward pass (copy path only)
+    MOE_CHECK(launch_gate_up_save(d, out->xs, x, out->offsets, w->gate_up, w->shared_gate_up, out->h,
+                                  out->h_shared, out->z, out->z_shared, workspace, st, q));
+  } else {
+    // xs == NULL: gate/up gathers the routed rows of x by TMA (no copies written by dispatch)
+    MOE_CHECK(launch_gate_up_perm(d, out->xs, x, out->offsets, out->xs ? nullptr : out->perm_tok, w->gate_up,
+                                  w->shared_gate_up, out->h, out->h_shared, workspace, st));
+  }
+  if (out->shared_out == nullptr)  // the combine runs in the down GEMM's shared-expert tiles
+    return launch_down_combine(d, out->offsets, out->h, out->h_shared, w->w_down, w->shared_down, out->ys,
+                               out->topk_gate, out->slot_row, out->topk_idx, x, w->const_vectors, out->y,
+                               workspace, st);
+  MOE_CHECK(launch_down(d, out->offsets, out->h, out->h_shared, w->w_down, w->shared_down, out->ys,
+                        out->shared_out, workspace, st));
+  // in place (shared_out == y): only the tokens the route listed as having a source
+  return launch_combine(d, out->ys, out->shared_out, out->topk_gate, out->slot_row, out->topk_idx, x,
+                        w->const_vectors, out->y, st, out->shared_out == out->y ? workspace : nullptr);
+}
+
 extern "C" {
 
 int moe_abi_version(void) { return MOE_NULL_ABI_VERSION; }
@@ -276,39 +316,32 @@ int moe_forward(const moe_dims_t* dims, const moe_weights_t* w, const uint16_t* 
                 const moe_outputs_t* out, void* workspace, moe_stream_t stream) {
   MOE_CHECK(check_dims(dims));
   if (dims->T == 0) return MOE_OK;
-  if (!w || !out || !x || !workspace) return MOE_ERR_INVALID_ARG;
-  if (!w->w_router || !w->gate_up || !w->w_down || !w->shared_gate_up || !w->shared_down)
-    return MOE_ERR_INVALID_ARG;
-  if (dims->V > 0 && !w->const_vectors) return MOE_ERR_INVALID_ARG;
-  if (!out->topk_idx || !out->topk_gate || !out->n_real || !out->counts || !out->offsets || !out->perm_tok ||
-      !out->slot_row || !out->h || !out->h_shared || !out->ys || !out->y || !out->counts_ext || !out->P ||
-      !out->losses)
-    return MOE_ERR_INVALID_ARG;
+  MOE_CHECK(check_forward(dims, w, x, out, workspace));
   // saved pre-activations: both buffers or neither, and only with the gathered copy xs
   if ((out->z != nullptr) != (out->z_shared != nullptr) || (out->z && !out->xs)) return MOE_ERR_INVALID_ARG;
+  return forward_run(*dims, w, x, tok_null_bias, out, nullptr, workspace, S(stream));
+}
+
+int moe_forward_checkpoint8(const moe_dims_t* dims, const moe_weights_t* w, const uint16_t* x,
+                            const float* tok_null_bias, const moe_outputs_t* out, const moe_codes8_t* codes,
+                            void* workspace, moe_stream_t stream) {
+  MOE_CHECK(check_dims(dims));
+  if (dims->T == 0) return MOE_OK;
+  MOE_CHECK(check_forward(dims, w, x, out, workspace));
+  if (!out->xs || !out->logits || !codes) return MOE_ERR_INVALID_ARG;
+  const moe_codes8_t& q = *codes;
+  if (!q.z_codes || !q.z_scales || !q.zs_codes || !q.zs_scales || !q.ys_codes || !q.ys_scales)
+    return MOE_ERR_INVALID_ARG;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(q.z_codes) | reinterpret_cast<uintptr_t>(q.zs_codes) |
+                       reinterpret_cast<uintptr_t>(q.ys_codes);
+  const uintptr_t sc = reinterpret_cast<uintptr_t>(q.z_scales) | reinterpret_cast<uintptr_t>(q.zs_scales) |
+                       reinterpret_cast<uintptr_t>(q.ys_scales);
+  if (at % 16 != 0 || sc % 4 != 0) return MOE_ERR_INVALID_ARG;
+  const moe_dims_t& d = *dims;
   const cudaStream_t st = S(stream);
-  MOE_CHECK(launch_route(*dims, x, w->w_router, w->router_bias, tok_null_bias, out->logits, out->topk_idx,
-                         out->topk_gate, out->n_real, workspace, st, w->router_split));
-  MOE_CHECK(launch_dispatch(*dims, x, out->topk_idx, workspace, out->counts, out->offsets, out->perm_tok,
-                            out->slot_row, out->xs, out->counts_ext, out->P, out->losses, st));
-  if (out->z) {
-    // training: the pre-activations are kept for the backward pass (copy path only)
-    MOE_CHECK(launch_gate_up_save(*dims, out->xs, x, out->offsets, w->gate_up, w->shared_gate_up, out->h,
-                                  out->h_shared, out->z, out->z_shared, workspace, st));
-  } else {
-    // xs == NULL: gate/up gathers the routed rows of x by TMA (no copies written by dispatch)
-    MOE_CHECK(launch_gate_up_perm(*dims, out->xs, x, out->offsets, out->xs ? nullptr : out->perm_tok, w->gate_up,
-                                  w->shared_gate_up, out->h, out->h_shared, workspace, st));
-  }
-  if (out->shared_out == nullptr)  // the combine runs in the down GEMM's shared-expert tiles
-    return launch_down_combine(*dims, out->offsets, out->h, out->h_shared, w->w_down, w->shared_down, out->ys,
-                               out->topk_gate, out->slot_row, out->topk_idx, x, w->const_vectors, out->y,
-                               workspace, st);
-  MOE_CHECK(launch_down(*dims, out->offsets, out->h, out->h_shared, w->w_down, w->shared_down, out->ys,
-                        out->shared_out, workspace, st));
-  // in place (shared_out == y): only the tokens the route listed as having a source
-  return launch_combine(*dims, out->ys, out->shared_out, out->topk_gate, out->slot_row, out->topk_idx, x,
-                        w->const_vectors, out->y, st, out->shared_out == out->y ? workspace : nullptr);
+  MOE_CHECK(forward_run(d, w, x, tok_null_bias, out, codes, workspace, st));
+  return launch_checkpoint8((long long)d.T * d.K, d.d, MOE_DTYPE_BF16, out->ys, d.d, out->offsets + d.N, q.ys_codes,
+                            q.ys_scales, ws_ptr<uint32_t>(workspace, ws_layout(d).hdr), st);
 }
 
 int moe_get_device_status(const void* workspace, moe_stream_t stream) {

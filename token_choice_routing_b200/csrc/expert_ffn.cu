@@ -40,7 +40,7 @@
 // MMA thread fences them into the async proxy before issuing. Rows past the
 // expert's end read token 0 and are never stored. Dispatch then writes no row
 // copies at all.
-#include "moe_internal.cuh"
+#include "rows.cuh"
 
 #include <cudaTypedefs.h>
 #include <mutex>
@@ -74,6 +74,10 @@ struct GemmArgs {
   int ldz_r;
   uint16_t* zout_s;        // SAVEZ: the shared expert's [T, 2F_shared]
   int ldz_s;
+  int8_t* qz_r;            // SAVEZ 2: the pre-activations in 8-bit blocks instead (rows of ldz codes
+  uint8_t* qz_scale_r;     // and ldz / 32 scale bytes)
+  int8_t* qz_s;
+  uint8_t* qz_scale_s;
   // COMBINE: the shared tiles' epilogue writes y from the shared expert's output and the
   // token's slots (source of slot k: slot_row >= 0 a row of out_r = ys; else, with MoE++
   // experts, topk_idx tells a copy expert (row of cx) or constant expert j (row j of cv))
@@ -194,7 +198,7 @@ __device__ __forceinline__ void combine_chunk(const GemmArgs& a, const uint32_t 
                         pack_bf16x2(acc[8 * j + 4], acc[8 * j + 5]), pack_bf16x2(acc[8 * j + 6], acc[8 * j + 7]));
 }
 
-template <int BN, bool SWIGLU, bool GATHER, bool SAVEZ = false, bool COMBINE = false>
+template <int BN, bool SWIGLU, bool GATHER, int SAVEZ = 0, bool COMBINE = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA_r, const __grid_constant__ CUtensorMap tmB_r,
                     const __grid_constant__ CUtensorMap tmA_s, const __grid_constant__ CUtensorMap tmB_s,
@@ -503,6 +507,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA_r, const __grid_cons
       const int ld = (ti.g < N) ? a.ld_r : a.ld_s;
 #pragma unroll 1
       for (int c = 0; c < NCHUNK; ++c) {
+        [[maybe_unused]] uint32_t zg[16], zu[16], zscale = 0;  // SAVEZ 2: a block of gate and one of up columns
 #pragma unroll
         for (int g16 = 0; g16 < 4; ++g16) {
           uint32_t packed[8];
@@ -519,7 +524,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA_r, const __grid_cons
               const float h1 = __fdividef(g1, 1.f + __expf(-g1)) * u1;
               packed[j] = pack_bf16x2(h0, h1);
             }
-            if constexpr (SAVEZ) {
+            if constexpr (SAVEZ == 1) {
               // training: keep the pre-activations (bf16, packed order) for the backward pass
               if (row < ti.mvalid) {
                 uint16_t* zo = (ti.g < N) ? a.zout_r : a.zout_s;
@@ -538,6 +543,23 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA_r, const __grid_cons
                                      pack_bf16x2(__uint_as_float(ur[8 * q + 4]), __uint_as_float(ur[8 * q + 5])),
                                      pack_bf16x2(__uint_as_float(ur[8 * q + 6]), __uint_as_float(ur[8 * q + 7])));
                 }
+              }
+            }
+            if constexpr (SAVEZ == 2) {
+              // training with 8-bit checkpoints: the same bf16 values as blocks of 32 columns
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                zg[(g16 & 1) * 8 + j] = pack_bf16x2(__uint_as_float(gr[2 * j]), __uint_as_float(gr[2 * j + 1]));
+                zu[(g16 & 1) * 8 + j] = pack_bf16x2(__uint_as_float(ur[2 * j]), __uint_as_float(ur[2 * j + 1]));
+              }
+              if ((g16 & 1) && row < ti.mvalid) {
+                const bool routed = ti.g < N;
+                const int ldz = routed ? a.ldz_r : a.ldz_s;
+                const size_t at = (size_t)(ti.arow + row) * ldz + 2 * ti.col0 + c * 128;
+                int8_t* q = (routed ? a.qz_r : a.qz_s) + at + (g16 >> 1) * 32;
+                zscale |= store_block8(zg, q) << ((g16 >> 1) * 8);
+                zscale |= store_block8(zu, q + 64) << (16 + (g16 >> 1) * 8);
+                if (g16 == 3) *reinterpret_cast<uint32_t*>((routed ? a.qz_scale_r : a.qz_scale_s) + at / 32) = zscale;
               }
             }
           } else {
@@ -660,7 +682,7 @@ bool make_tmap_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t col
   return r == CUDA_SUCCESS;
 }
 
-template <int BN, bool SWIGLU, bool GATHER, bool SAVEZ = false, bool COMBINE = false>
+template <int BN, bool SWIGLU, bool GATHER, int SAVEZ = 0, bool COMBINE = false>
 static int launch_gemm(const CUtensorMap& ar, const CUtensorMap& br, const CUtensorMap& as_,
                        const CUtensorMap& bs, const GemmArgs& a, long long max_tiles, cudaStream_t st) {
   using SM = GemmSmem<BN>;
@@ -762,10 +784,10 @@ int launch_gate_up_perm(const moe_dims_t& d, const uint16_t* xs, const uint16_t*
 }
 
 // gate/up with the pre-activations also written (training): z [rows_cap, 2F] and zs [T, 2F_shared]
-// in the packed column order, bf16. Copy path (xs) only.
+// in the packed column order, bf16, or with q their 8-bit blocks instead. Copy path (xs) only.
 int launch_gate_up_save(const moe_dims_t& d, const uint16_t* xs, const uint16_t* x, const int32_t* offsets,
                         const uint16_t* gate_up, const uint16_t* sgate_up, uint16_t* h, uint16_t* h_shared,
-                        uint16_t* z, uint16_t* zs, void* ws, cudaStream_t st) {
+                        uint16_t* z, uint16_t* zs, void* ws, cudaStream_t st, const moe_codes8_t* q) {
   FfnPlan p = plan_ffn(d, offsets, ws);
   const long long rcap = (long long)d.T * d.K;
   CUtensorMap ar, br, as_, bs;
@@ -782,8 +804,16 @@ int launch_gate_up_save(const moe_dims_t& d, const uint16_t* xs, const uint16_t*
   p.g1.ldz_r = 2 * d.F;
   p.g1.zout_s = zs;
   p.g1.ldz_s = 2 * d.F_shared;
-  return (p.BN1 == 256) ? launch_gemm<256, true, false, true>(ar, br, as_, bs, p.g1, p.max1, st)
-                        : launch_gemm<128, true, false, true>(ar, br, as_, bs, p.g1, p.max1, st);
+  if (q) {
+    p.g1.qz_r = q->z_codes;
+    p.g1.qz_scale_r = q->z_scales;
+    p.g1.qz_s = q->zs_codes;
+    p.g1.qz_scale_s = q->zs_scales;
+    return (p.BN1 == 256) ? launch_gemm<256, true, false, 2>(ar, br, as_, bs, p.g1, p.max1, st)
+                          : launch_gemm<128, true, false, 2>(ar, br, as_, bs, p.g1, p.max1, st);
+  }
+  return (p.BN1 == 256) ? launch_gemm<256, true, false, 1>(ar, br, as_, bs, p.g1, p.max1, st)
+                        : launch_gemm<128, true, false, 1>(ar, br, as_, bs, p.g1, p.max1, st);
 }
 
 int launch_down(const moe_dims_t& d, const int32_t* offsets, const uint16_t* h, const uint16_t* h_shared,
@@ -835,8 +865,8 @@ int launch_down_combine(const moe_dims_t& d, const int32_t* offsets, const uint1
   g.V = d.V;
   g.tiles_done = ws_ptr<uint32_t>(ws, L.hdr + kHdrCombineOffset);
   g.cta_exits = g.tiles_done + 1;
-  return (p.BN2 == 256) ? launch_gemm<256, false, false, false, true>(ar, br, as_, bs, g, p.max2, st)
-                        : launch_gemm<128, false, false, false, true>(ar, br, as_, bs, g, p.max2, st);
+  return (p.BN2 == 256) ? launch_gemm<256, false, false, 0, true>(ar, br, as_, bs, g, p.max2, st)
+                        : launch_gemm<128, false, false, 0, true>(ar, br, as_, bs, g, p.max2, st);
 }
 
 // Expert parallelism: the grouped GEMMs of one rank's expert shard over the rows it

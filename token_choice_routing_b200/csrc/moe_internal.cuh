@@ -272,10 +272,10 @@ int launch_expert_ffn(const moe_dims_t& d, const uint16_t* xs, const uint16_t* x
                       uint16_t* h_shared, uint16_t* ys, uint16_t* shared_out, void* ws,
                       cudaStream_t st);
 // gate/up that also writes the pre-activations z [T K, 2F] and zs [T, 2F_shared] (bf16, packed
-// column order) for the backward pass; copy path (xs) only
+// column order) for the backward pass, or with q their 8-bit blocks; copy path (xs) only
 int launch_gate_up_save(const moe_dims_t& d, const uint16_t* xs, const uint16_t* x, const int32_t* offsets,
                         const uint16_t* gate_up, const uint16_t* sgate_up, uint16_t* h, uint16_t* h_shared,
-                        uint16_t* z, uint16_t* zs, void* ws, cudaStream_t st);
+                        uint16_t* z, uint16_t* zs, void* ws, cudaStream_t st, const moe_codes8_t* q = nullptr);
 int launch_gate_up(const moe_dims_t& d, const uint16_t* xs, const uint16_t* x, const int32_t* offsets,
                    const uint16_t* gate_up, const uint16_t* sgate_up, uint16_t* h, uint16_t* h_shared,
                    void* ws, cudaStream_t st);

@@ -163,6 +163,72 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
+// ---- 8-bit blocks: 32 columns with one power-of-two scale (the format is described in ckpt8.cu)
+constexpr uint32_t kByteNan = 255u;
+
+// Scale byte of a block from its largest magnitude's fp32 bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
+  const uint32_t e = top_bits >> 23;
+  return e == 255u ? kByteNan : max((int)e - 6, 1);
+}
+// 2^-E (finite blocks: bytes 1 .. 248).
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
+
+// rint(x 2^-E) as the low 16 bits of 1.5 2^23 + code: the product is exact, so the addition's
+// rounding to nearest even is the only one. |x 2^-E| < 128: the code is in [-128, 128] before the
+// clamp, which is taken on two 16-bit codes at a time.
+constexpr float kRoundBias = 12582912.f;
+__device__ __forceinline__ uint32_t quantise(float x, float inv) { return __float_as_uint(fmaf(x, inv, kRoundBias)); }
+__device__ __forceinline__ uint32_t clamp2(uint32_t two) {
+  return __vmaxs2(__vmins2(two, 0x007f007fu), 0xff81ff81u);
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(clamp2(__byte_perm(a, b, 0x5410)), clamp2(__byte_perm(c, d, 0x5410)), 0x6420);
+}
+
+// Bits of the largest magnitude among the elements of a piece, as fp32 bits. The 16-bit types are
+// compared as bits, two at a time: magnitudes order as their bits do, infinity and NaN on top.
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_of(const Piece<E, V>& p) {
+  if constexpr (V == 4) {
+    return max(max(p.w.x & 0x7fffffffu, p.w.y & 0x7fffffffu), max(p.w.z & 0x7fffffffu, p.w.w & 0x7fffffffu));
+  } else {
+    return __vmaxu2(__vmaxu2(p.w.x & 0x7fff7fffu, p.w.y & 0x7fff7fffu),
+                    __vmaxu2(p.w.z & 0x7fff7fffu, p.w.w & 0x7fff7fffu));
+  }
+}
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_join(uint32_t a, uint32_t b) {
+  return V == 4 ? max(a, b) : __vmaxu2(a, b);
+}
+template <typename E, int V>
+__device__ __forceinline__ uint32_t top_bits(uint32_t t) {
+  if constexpr (V == 4) {
+    return t;
+  } else {
+    return __float_as_uint(word_to_float2<E>(max(t & 0xffffu, t >> 16)).x);
+  }
+}
+
+// One block from 32 bf16 values in 16 words: its codes to a 16-byte boundary; returns the scale byte.
+__device__ __forceinline__ uint32_t store_block8(const uint32_t (&w)[16], int8_t* codes) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+  const uint32_t byte = scale_byte(max(top & 0xffffu, top >> 16) << 16);
+  const float inv = scale_inverse(byte);
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    q[j] = pack4(quantise(bf16lo(w[2 * j]), inv), quantise(bf16hi(w[2 * j]), inv), quantise(bf16lo(w[2 * j + 1]), inv),
+                 quantise(bf16hi(w[2 * j + 1]), inv));
+    if (byte == kByteNan) q[j] = 0u;
+  }
+  reinterpret_cast<uint4*>(codes)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+  reinterpret_cast<uint4*>(codes)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  return byte;
+}
+
 #endif  // __CUDACC__
 
 }  // namespace moe

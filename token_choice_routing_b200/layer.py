@@ -236,8 +236,8 @@ class MoENullLayer:
         """What one forward leaves for its backward in 8 bits: the gate/up pre-activations and
         the routed outputs as codes with a scale byte per 32 columns, and the routing as it is.
         Per routed slot that is (2 F + d) 33/32 bytes in the place of the 6 F + 4 d that z, h, xs
-        and ys take in bf16, which the layers of a model then share as scratch
-        (``alloc(T, save_preact=True)`` once)."""
+        and ys take in bf16; z is never written in bf16, and h, xs and ys are scratch that the
+        layers of a model share (``alloc(T)`` once)."""
         dev, d, N, M, K, F, Fs = self.device, self.d, self.N, self.M, self.K, self.F, self.F_shared
         R, T1 = max(T * K, 1), max(T, 1)
         i32, f32, i8, u8 = torch.int32, torch.float32, torch.int8, torch.uint8
@@ -257,24 +257,20 @@ class MoENullLayer:
     def forward_checkpoint8(self, x: torch.Tensor, tok_null_bias: Optional[torch.Tensor],
                             out: Dict[str, torch.Tensor], ck: Dict[str, torch.Tensor],
                             stream=None) -> Dict[str, torch.Tensor]:
-        """The forward, keeping for the backward only ``ck`` (``alloc_checkpoint8``) and x. ``out``
-        (``alloc(T, save_preact=True)``) is scratch that the next layer's forward may use; its
-        buffers of the routing are left alone and the checkpoint's taken. Returns the outputs as
-        ``forward`` does."""
+        """The forward, keeping for the backward only ``ck`` (``alloc_checkpoint8``) and x
+        (``moe_forward_checkpoint8``). ``out`` (``alloc(T)``) is scratch that the next layer's forward
+        may use; its buffers of the routing are left alone and the checkpoint's taken. Returns the
+        outputs as ``forward`` does."""
         T = x.shape[0]
-        R = T * self.K
-        if out.get("z") is None or out.get("xs") is None or out["z"].shape[0] < R or out["y"].shape[0] < T:
-            raise ValueError("an 8-bit checkpoint needs out from alloc(T, save_preact=True)")
+        if out.get("xs") is None or out["xs"].shape[0] < T * self.K or out["y"].shape[0] < T:
+            raise ValueError(f"an 8-bit checkpoint needs out from alloc({T}) with xs")
         if ck["slot_row"].shape[0] < T:
             raise ValueError(f"the checkpoint holds {ck['slot_row'].shape[0]} tokens, not {T}")
         o = dict(out)
         o.update({n: ck[n] for n in B.SAVED8_FIELDS if n != "x"})
-        self.forward(x, tok_null_bias, o, stream)
-        if T > 0:
-            ws, used = o["workspace"], o["offsets"][self.N:]
-            B.checkpoint8(o["z"][:R], ck["z_codes"][:R], ck["z_scales"][:R], used, ws, stream)
-            B.checkpoint8(o["z_shared"][:T], ck["zs_codes"][:T], ck["zs_scales"][:T], None, ws, stream)
-            B.checkpoint8(o["ys"][:R], ck["ys_codes"][:R], ck["ys_scales"][:R], used, ws, stream)
+        ob = B.Outputs(*[None if o.get(n) is None else o[n].data_ptr() for n in B.OUTPUT_FIELDS])
+        q = B.Codes8(*[ck[n].data_ptr() for n in B.SAVED8_CODES])
+        B.forward_checkpoint8(self.dims(T), self._weights, x, tok_null_bias, ob, q, o["workspace"], stream)
         return o
 
     def backward_checkpoint8(self, x: torch.Tensor, ck: Dict[str, torch.Tensor], dy: torch.Tensor,

@@ -47,8 +47,7 @@ def main(argv=None) -> int:
     layer = MoENullLayer.from_inputs(inp, "cuda", router=a.router, ffn=a.ffn)
     x = bf16_tensor(inp.x, "cuda")
     tnb = None if inp.tok_null_bias is None else torch.from_numpy(inp.tok_null_bias).cuda()
-    out = layer.alloc(inp.cfg.T, logits=a.backwards > 0, save_preact=a.save_preact or a.checkpoint8,
-                      combine=a.combine)
+    out = layer.alloc(inp.cfg.T, logits=a.backwards > 0, save_preact=a.save_preact, combine=a.combine)
     ck = layer.alloc_checkpoint8(inp.cfg.T) if a.checkpoint8 else None
     for _ in range(a.forwards):
         if a.checkpoint8:
