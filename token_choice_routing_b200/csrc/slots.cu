@@ -73,11 +73,12 @@ struct SortArgs {
   int N, chunks;
 };
 
-// The slot's expert, -1 for none.
+// The slot's expert, -1 for none. Read past the L1 cache: the placing kernel reads the ids before it
+// waits for its predecessor.
 template <typename Id>
 __device__ __forceinline__ int sort_id(const SortArgs& a, long long s, long long end) {
   if (s >= end) return -1;
-  const Id v = __ldg(static_cast<const Id*>(a.ids) + s);
+  const Id v = __ldcg(static_cast<const Id*>(a.ids) + s);
   return (v >= 0 && v < (Id)a.N) ? (int)v : -1;
 }
 
@@ -730,6 +731,8 @@ __global__ void __launch_bounds__(kRowThreads) spread_dot_narrow_kernel(RowArgs 
   }
 }
 
+static unsigned blocks_for(long long n, int per_block) { return (unsigned)((n + per_block - 1) / per_block); }
+
 // Chunks per token and the grid over them; false when the index space is too large for any
 // buffer of this GPU's memory.
 static bool row_items(RowArgs& a, int chunk) {
@@ -751,11 +754,11 @@ template <typename E, int V, int NV>
 static int collect_go(RowArgs a, cudaStream_t st) {
   if (a.d <= kNarrow<V>) {
     if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
-    return launch_pdl(collect_narrow_kernel<E, V>, dim3((a.items + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0,
+    return launch_pdl(collect_narrow_kernel<E, V>, dim3(blocks_for(a.items, kRowThreads)), dim3(kRowThreads), 0,
                       st, a);
   }
   if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
-  return launch_pdl(collect_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
+  return launch_pdl(collect_kernel<E, V, NV>, dim3(blocks_for(a.items, kRowWarps)), dim3(kRowThreads), 0, st, a);
 }
 
 template <typename E>
@@ -771,11 +774,11 @@ template <typename E, int V, int NV>
 static int spread_go(RowArgs a, cudaStream_t st) {
   if (a.d <= kNarrow<V>) {
     if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
-    return launch_pdl(spread_narrow_kernel<E, V>, dim3((a.items + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0,
+    return launch_pdl(spread_narrow_kernel<E, V>, dim3(blocks_for(a.items, kRowThreads)), dim3(kRowThreads), 0,
                       st, a);
   }
   if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
-  return launch_pdl(spread_kernel<E, V, NV>, dim3((a.items + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, st, a);
+  return launch_pdl(spread_kernel<E, V, NV>, dim3(blocks_for(a.items, kRowWarps)), dim3(kRowThreads), 0, st, a);
 }
 
 template <typename E, int V, int NV, bool CODES>
@@ -784,15 +787,13 @@ static int spread_dot_go(const RowArgs& a, cudaStream_t st) {
     int G = 1;
     while (G * V < a.d) G *= 2;
     const int per_block = kRowThreads / G;
-    return launch_pdl(spread_dot_narrow_kernel<E, V, CODES>, dim3((a.T + per_block - 1) / per_block), dim3(kRowThreads),
+    return launch_pdl(spread_dot_narrow_kernel<E, V, CODES>, dim3(blocks_for(a.T, per_block)), dim3(kRowThreads),
                       0, st, a, G);
   }
   // more warps a token while the tokens alone do not fill the GPU and the row has chunks for them
   int wpt = 1;
   while (wpt < kRowWarps && (long long)a.T * wpt < (long long)sm_count() * 16 && a.d > wpt * 32 * V * NV) wpt *= 2;
-  const long long per_block = kRowWarps / wpt;
-  const dim3 grid((unsigned)((a.T + per_block - 1) / per_block));
-  return launch_pdl(spread_dot_kernel<E, V, NV, CODES>, grid, dim3(kRowThreads), 0, st, a, wpt);
+  return launch_pdl(spread_dot_kernel<E, V, NV, CODES>, dim3(blocks_for(a.T, kRowWarps / wpt)), dim3(kRowThreads), 0, st, a, wpt);
 }
 
 template <typename E>
