@@ -607,8 +607,9 @@ typedef enum {
   MOE_DTYPE_F32 = 2
 } moe_dtype_t;
 
-/* Workspace of moe_sort_slots in bytes (0 if the sizes are invalid): 256 + 4 N bytes per chunk of
- * the slots, at most 148 chunks. Its first word is a status word that the sort clears. */
+/* Workspace of moe_sort_slots in bytes (0 if the sizes are invalid): 256, and 4 N bytes for each of at
+ * most 148 chunks of the slots. Its first word is a status word that the sort clears. One
+ * workspace serves one sort at a time. */
 MOE_API size_t moe_sort_workspace_bytes(int32_t T, int32_t K, int32_t N);
 
 /* Stable counting sort of the T*K slots by expert id (1 <= N <= 1024). ids [T, K] int32

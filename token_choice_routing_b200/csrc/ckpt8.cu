@@ -10,6 +10,16 @@
 // error is at most 2^(E-1), except above 127.5 2^E (a bf16 block reaches exactly 127.5), where
 // the clamp leaves less than 2^E. A block with an infinity or a NaN gets byte 255 and is
 // restored as NaN throughout, so that an overflow in the forward shows in the gradient.
+//
+// All three are one pass over HBM and bound by it at the layer's sizes (bf16, copy rate 6.5 TB/s):
+//   store   32768 x 1536  25.2 us  6.1 TB/s      131072 x 1536  96 us  6.3 TB/s
+//   restore 32768 x 1536  26.9 us  5.7 TB/s      131072 x 1536 106 us  5.7 TB/s
+//   SwiGLU  32768 x 768   45.0 us  5.6 TB/s      104857 x 1024 175 us  6.2 TB/s
+// The two that write more than they read stay further from the copy rate, which reads as much.
+// Getting there took the integer instructions out (68% of the ALU pipe at first): maxima, clamps
+// and packing on two or four values at a time, no index arithmetic for dense tensors. Rows that no
+// 16-byte access fits take one element a lane and stay bound by instructions: 60000 x 1001 store
+// and restore 137 us (2.6 TB/s), SwiGLU's backward of 60000 x 499 90 us (3.4 TB/s).
 #include "rows.cuh"
 
 #include <algorithm>
@@ -19,6 +29,7 @@ namespace moe {
 constexpr int kCkptThreads = 256;
 constexpr int kCkptCtas = 8;     // CTAs of the grid a multiprocessor
 constexpr int kSwigluCtas = 16;
+
 // Rows in use: *used clamped to [0, rows] (recorded when it lies outside), or all of them.
 __device__ __forceinline__ long long rows_in_use(const int32_t* used, long long rows, uint32_t* status) {
   if (!used) return rows;
@@ -128,7 +139,8 @@ struct Spot {
 
 // Store, rows of 16-byte pieces: an item is half a block, two neighbouring lanes a block (a row
 // has 2 nb items; columns past its end stand for zeros). kUnroll items a thread are loaded before
-// any is used.
+// any is used: four with two CTAs a multiprocessor 25.1 us for 32768 x 1536, two 25.6, one 29.2; a
+// quarter of a block an item 37 us.
 constexpr int kItem = 16;
 constexpr int kUnroll = 4;
 template <typename E, bool FLAT>
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kCkptThreads) checkpoint8_elem_kernel(Ckpt8Arg
 
 // Restore, rows of 16-byte pieces: an item is one of them, so that a warp's stores are whole
 // sectors (half a block a lane, as in the store, leaves 16 of every 32 bytes to a second
-// instruction: 28.8 against 27.3 us for 32768 x 1536 in bf16).
+// instruction: 28.8 us for 32768 x 1536). Eight items a thread 26.0 us, four 27.2, two 30.3.
 constexpr int kRestoreUnroll = 8;
 template <typename E, bool FLAT>
 __global__ void __launch_bounds__(kCkptThreads) restore8_kernel(Ckpt8Args a) {
@@ -344,7 +356,8 @@ __device__ __forceinline__ SwigluOut swiglu_grad(float a, float b, float g) {
 }
 
 // Rows of 16-byte pieces: an item is eight pairs. FLAT: dense rows in the packed order, where the
-// pair's number over the whole tensor gives all offsets; otherwise by its row.
+// pair's number over the whole tensor gives all offsets; otherwise by its row. Two items a thread
+// with three CTAs a multiprocessor 45 us for 32768 x 768; one with five 49, two with five 52.
 constexpr int kSwigluUnroll = 2;
 constexpr int kPairs = 8;
 template <bool FLAT>
@@ -455,7 +468,7 @@ __device__ __forceinline__ void swiglu_item(const Swiglu8Args& g, long long row,
   // lanes 0 .. kElemPairs-1: the gate blocks; from lane 16: the up blocks in order
   const int first_a = PACKED ? 2 * f0 / 32 : f0 / 32, first_b = PACKED ? first_a + 2 : (f0 + g.F) / 32;
   const int l = lane & 15;
-  const int blk = PACKED ? (lane < 16 ? first_a : first_b) + (l >> 1) * 4 + (l & 1) : (lane < 16 ? first_a : first_b) + l;
+  const int blk = (lane < 16 ? first_a : first_b) + (PACKED ? (l >> 1) * 4 + (l & 1) : l);
   const float sc = (l <= kElemPairs && blk < g.nb) ? scale_value(__ldg(scales + blk)) : 0.f;
   const int over = PACKED ? 0 : (((f0 + g.F) & 31) + lane) >> 5;  // 1: the lane's up columns lie in the next block
   E* dz = static_cast<E*>(g.dz) + row * g.lddz;

@@ -172,7 +172,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top_bits) {
   return e == 255u ? kByteNan : max((int)e - 6, 1);
 }
 // 2^-E (finite blocks: bytes 1 .. 248).
-__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+  return __uint_as_float((254u - min(byte, 253u)) << 23);
+}
 
 // rint(x 2^-E) as the low 16 bits of 1.5 2^23 + code: the product is exact, so the addition's
 // rounding to nearest even is the only one. |x 2^-E| < 128: the code is in [-128, 128] before the

@@ -439,7 +439,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) collect_kernel(RowArgs 
     collect_chunk<E, V, NV, false>(a, t, c0 + lane * V, row, w);
 }
 
-// rows_out[slot_row[t,k]] = w[t,k] tok[t] (w null: a copy).
+// rows_out[slot_row[t,k]] = w[t,k] tok[t] (w null: a copy). The row is read once and stays in
+// registers. Bound by HBM's writes: T = 65536, d = 2048, K = 8, half the slots null, bf16 205 us
+// (6.5 TB/s); T = 16384, d = 1024, K = 4 17.8 us (5.7 TB/s).
 template <typename E, int V, int NV>
 __global__ void __launch_bounds__(kRowThreads) spread_kernel(RowArgs a) {
   pdl_wait_then_release();
@@ -496,11 +498,15 @@ __device__ __forceinline__ float dot_codes(const float (&g)[V], const CodePiece<
 }
 
 // rows_out[slot_row[t,k]] = w[t,k] tok[t] (rows_out null: not written) and dw[t,k] = <tok[t],
-// rows_in[slot_row[t,k]]>, 0 for a slot without a row. WPT warps share a token, each every
-// WPT-th chunk of its columns; eight single elements of five rows a lane need more registers than
-// four CTAs leave (T = 16384, d = 1001, K = 4, bf16: 58 us with three CTAs, 94 with four; from codes
-// 79 us with two, 89 with three, 231 with four). A dot product is summed in fp32 per lane, over the lanes by a
-// fixed shuffle tree and over the warps in order, so it does not depend on timing.
+// rows_in[slot_row[t,k]]>, 0 for a slot without a row. wpt warps share a token, each every
+// wpt-th chunk of its columns. A dot product is summed in fp32 per lane, over the lanes by a fixed
+// shuffle tree and over the warps in order, so it does not depend on timing.
+// Bound by HBM: T = 65536, d = 2048, K = 8, half the slots null, bf16 375 us (6.5 TB/s), from codes
+// 315 us (6.0 TB/s); T = 16384 102 us; from codes at d = 1024, K = 4 29 us (4.7 TB/s), where a token
+// has two rows and a warp's chain of lookup, loads and stores is not covered. A persistent grid
+// that looks the next token's slots up ahead measured slower (375 -> 401 us and more).
+// Eight single elements of five rows a lane need more registers than four CTAs leave (T = 16384,
+// d = 1001, K = 4, bf16: 58 us with three CTAs, 94 with four; from codes 79 us with two, 231 with four).
 template <typename E, int V, int NV, bool CODES>
 __global__ void __launch_bounds__(kRowThreads, V == 1 && NV == kElemPieces ? (CODES ? 2 : 3) : kRowCtas)
     spread_dot_kernel(RowArgs a, int wpt) {
@@ -569,7 +575,8 @@ __global__ void __launch_bounds__(kRowThreads, V == 1 && NV == kElemPieces ? (CO
             float gf[V];
             g[v].get(gf);
             if constexpr (CODES && V == 1)  // before any lane leaves; columns past the row hold zeros
-              dot[u] = fmaf(gf[0] * (float)(int)q[u][v].word[0], __shfl_sync(0xffffffffu, lane_scale, u * NV + v), dot[u]);
+              dot[u] = fmaf(gf[0] * (float)(int)q[u][v].word[0], __shfl_sync(0xffffffffu, lane_scale, u * NV + v),
+                            dot[u]);
             if (c >= a.d) continue;
             if constexpr (CODES && V == 1) {
             } else if constexpr (CODES) {
@@ -792,8 +799,10 @@ static int spread_dot_go(const RowArgs& a, cudaStream_t st) {
   }
   // more warps a token while the tokens alone do not fill the GPU and the row has chunks for them
   int wpt = 1;
+  // (T = 64, d = 2048, K = 8: 3.9 us)
   while (wpt < kRowWarps && (long long)a.T * wpt < (long long)sm_count() * 16 && a.d > wpt * 32 * V * NV) wpt *= 2;
-  return launch_pdl(spread_dot_kernel<E, V, NV, CODES>, dim3(blocks_for(a.T, kRowWarps / wpt)), dim3(kRowThreads), 0, st, a, wpt);
+  return launch_pdl(spread_dot_kernel<E, V, NV, CODES>, dim3(blocks_for(a.T, kRowWarps / wpt)), dim3(kRowThreads), 0,
+                    st, a, wpt);
 }
 
 template <typename E>
