@@ -599,8 +599,9 @@ MOE_API int moe_backward(const moe_dims_t* dims, const moe_weights_t* w, const m
  * index at or past `rows` is skipped and sets MOE_ERR_DEVICE_BOUNDS in the status word at
  * the start of `status` (any workspace of this library, or 256 bytes of the caller's; NULL:
  * not recorded). Rows that no slot has are left as they were. Limits: 1 <= K <= 32,
- * T * K < 2^31, 1 <= d <= 2^30. Inputs and outputs must not overlap, except where said. T = 0
- * writes nothing but moe_sort_slots' counts and offsets. */
+ * T * K < 2^31, 1 <= d <= 2^30, rows >= 0 (0: no slot has a row; the row buffers may be NULL).
+ * Inputs and outputs must not overlap, except where said. T = 0 writes nothing but
+ * moe_sort_slots' counts and offsets. */
 typedef enum {
   MOE_DTYPE_BF16 = 0,
   MOE_DTYPE_F16 = 1,

@@ -120,8 +120,9 @@ def test_extreme_values_and_borders(dtype, cols):
     assert np.all(np.abs(val - f64(x))[fine] <= lim * step[fine])
 
 
-def test_rows_in_use():
-    rows, cols = 40, 72
+@pytest.mark.parametrize("cols", [45, 72, 96])
+def test_rows_in_use(cols):
+    rows = 40
     rng = np.random.default_rng(6)
     for dt in TYPES.values():
         x = spaced(rng, rows, cols, dt)
@@ -129,16 +130,32 @@ def test_rows_in_use():
         for used in (0, 1, 30):
             n = torch.tensor([used], dtype=torch.int32, device="cuda")
             codes = torch.full((rows, cols), 5, dtype=torch.int8, device="cuda")
-            scales = torch.full((rows, 3), 7, dtype=torch.uint8, device="cuda")
+            nb = B.checkpoint8_scales(cols)
+            scales = torch.full((rows, nb), 7, dtype=torch.uint8, device="cuda")
             ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
             B.checkpoint8(x, codes, scales, n, ws)
-            val, byte = stored_ref(f64(x[:used])) if used else (np.empty((0, cols)), np.empty((0, 3)))
+            val, byte = stored_ref(f64(x[:used])) if used else (np.empty((0, cols)), np.empty((0, nb)))
             assert np.array_equal(scales[:used].cpu().numpy(), byte)
             assert bool((codes[used:] == 5).all()) and bool((scales[used:] == 7).all())
             back = torch.full((rows, cols), 2.0, dtype=dt, device="cuda")
             B.restore8(codes, scales, back, n, ws)
             assert np.array_equal(f64(back[:used]), val) and bool((back[used:] == 2.0).all())
             assert B.get_device_status(ws) == B.OK
+
+
+def test_restored_in_another_type_than_stored():
+    """Values have at most 7 significant bits: exact in every type whose range they lie in."""
+    rng = np.random.default_rng(9)
+    for src in TYPES.values():
+        for cols in (64, 40, 33):
+            x = spaced(rng, 30, cols, src)
+            codes = torch.empty((30, cols), dtype=torch.int8, device="cuda")
+            scales = torch.empty((30, B.checkpoint8_scales(cols)), dtype=torch.uint8, device="cuda")
+            B.checkpoint8(x, codes, scales)
+            for dst in TYPES.values():
+                back = torch.empty((30, cols), dtype=dst, device="cuda")
+                B.restore8(codes, scales, back)
+                assert np.array_equal(f64(back), stored_ref(f64(x))[0])
 
 
 def test_rows_in_use_outside_the_buffer_are_clamped_and_recorded():
@@ -206,6 +223,12 @@ def test_swiglu_backward8(rows, F, packed, dtype):
         dz2 = torch.empty((rows, 2 * F), dtype=dt, device="cuda")
         B.swiglu_backward8(codes, scales, dh, dz2, None, packed=packed)       # without h
         assert torch.equal(dz2, dz)
+        used = rows // 2
+        n = torch.tensor([used], dtype=torch.int32, device="cuda")
+        dz3, h3 = spaced(rng, rows, 2 * F, dt, pad, lead, fill=9.0), spaced(rng, rows, F, dt, pad, lead, fill=9.0)
+        B.swiglu_backward8(codes, scales, dh, dz3, h3, packed=packed, rows_used=n)
+        assert torch.equal(dz3[:used], dz[:used]) and torch.equal(h3[:used], h[:used])
+        assert bool((dz3[used:] == 9.0).all()) and bool((h3[used:] == 9.0).all())
 
 
 def test_swiglu_backward8_extremes():

@@ -120,7 +120,7 @@ def test_sort_matches_the_layer_dispatch():
 
 # --------------------------------------------------------------------------- row movement
 
-SHAPES = [(1, 1, 1, 1), (1, 8, 64, 2048), (3, 2, 4, 7), (33, 5, 9, 100), (64, 4, 16, 256), (130, 32, 40, 33),
+SHAPES = [(1, 1, 1, 1), (1, 8, 64, 2048), (2, 4, 8, 8192), (3, 2, 4, 7), (33, 5, 9, 100), (70, 32, 50, 640), (64, 4, 16, 256), (130, 32, 40, 33),
           (257, 3, 7, 1001), (300, 8, 64, 1024), (2000, 6, 64, 72), (511, 16, 300, 520)]
 
 
@@ -338,6 +338,75 @@ def test_rows_past_the_buffer_are_skipped_and_recorded():
             call(sr, a, ws)
             assert B.get_device_status(ws) == B.ERR_DEVICE_BOUNDS
             assert torch.equal(a, b) and torch.equal(dw, dwb)
+
+
+def test_without_rows_only_the_token_side_is_written():
+    """No slot has a row and the row buffers are empty, as on a rank that received nothing."""
+    T, K, d = 5, 3, 96
+    for dt in TYPES.values():
+        none = torch.zeros((0, d), dtype=dt, device="cuda")
+        sr = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+        x = torch.randn((T, d), device="cuda").to(dt)
+        w, dw = torch.full((T, K), float("nan"), device="cuda"), torch.full((T, K), 7.0, device="cuda")
+        y = torch.full_like(x, 9.0)
+        B.permute(x, sr, none)
+        B.unpermute(none, w, sr, y, base=x)
+        assert torch.equal(y, x)
+        B.permute_backward(none, sr, y)
+        assert not bool(y.any())
+        B.unpermute_backward(x, none, w, sr, none, dw)
+        assert not bool(dw.any())
+        codes, scales = none.to(torch.int8), torch.zeros((0, 3), dtype=torch.uint8, device="cuda")
+        dw.fill_(7.0)
+        B.unpermute_backward8(x, codes, scales, w, sr, None, dw)
+        assert not bool(dw.any())
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        sr[2, 1] = 0                                       # a row that does not exist
+        B.permute(x, sr, none, ws)
+        assert B.get_device_status(ws) == B.ERR_DEVICE_BOUNDS
+
+
+def test_a_stream_passed_to_the_call():
+    T, K, N, d = 900, 4, 20, 128
+    rng = np.random.default_rng(21)
+    side = torch.cuda.Stream()
+    ids = draw_ids(rng, T, K, N, 0.3)
+    x = torch.randn((T, d), device="cuda").to(torch.bfloat16)
+    w = torch.rand((T, K), device="cuda")
+    o = run_sort(ids, N)
+    want = torch.zeros((T * K, d), dtype=torch.bfloat16, device="cuda")
+    y_want = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    B.permute(x, o["slot_row"], want)
+    B.unpermute(want, w, o["slot_row"], y_want)
+    ws = torch.empty(B.sort_workspace_bytes(T, K, N), dtype=torch.uint8, device="cuda")
+    got = {n: torch.empty_like(v) for n, v in o.items()}
+    xs, y = torch.zeros_like(want), torch.zeros_like(y_want)
+    torch.cuda.synchronize()
+    B.sort_slots(ids, N, got["counts"], got["offsets"], got["perm_tok"], got["slot_row"], ws, side)
+    B.permute(x, got["slot_row"], xs, ws, side)
+    B.unpermute(xs, w, got["slot_row"], y, ws=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(got["slot_row"], o["slot_row"]) and torch.equal(xs, want) and torch.equal(y, y_want)
+
+
+@pytest.mark.parametrize("T,K,N", [(40, 4, 1024), (3000, 8, 1024), (20000, 8, 700)])
+def test_captured_sorts_of_many_experts(T, K, N):
+    """The sort's larger shared memory and its two launches under capture, on changing ids."""
+    rng = np.random.default_rng(T)
+    ids = draw_ids(rng, T, K, N, 0.2)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    o = dict(counts=z(N), offsets=z(N + 1), perm=z(T * K), row=z(T, K))
+    ws = torch.empty(B.sort_workspace_bytes(T, K, N), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        B.sort_slots(ids, N, o["counts"], o["offsets"], o["perm"], o["row"], ws)
+    for _ in range(4):
+        ids.copy_(draw_ids(rng, T, K, N, 0.2))
+        g.replay()
+        counts, offsets, perm, row = sort_ref(ids.cpu().numpy(), N)
+        assert np.array_equal(o["row"].cpu().numpy(), row) and np.array_equal(o["offsets"].cpu().numpy(), offsets)
+        assert np.array_equal(o["perm"][:int(offsets[-1])].cpu().numpy(), perm)
 
 
 def test_rows_beyond_32_bit_offsets():

@@ -58,7 +58,8 @@ int moe_permute(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype, co
   const int r = check_rows(T, K, rows, d, dtype);
   if (r != MOE_OK) return r;
   if (T == 0) return MOE_OK;
-  if (!x || !slot_row || !xs || ldx < d || ldxs < d) return MOE_ERR_INVALID_ARG;
+  if (!x || !slot_row || (rows > 0 && !xs) || ldx < d || ldxs < d) return MOE_ERR_INVALID_ARG;
+  if (rows == 0 && !status) return MOE_OK;  // nothing to write, nowhere to record a bad index
   return launch_spread(T, K, rows, d, dtype, x, ldx, nullptr, 0, nullptr, nullptr, slot_row, xs, ldxs, nullptr,
                        status_word(status), S(stream));
 }
@@ -69,7 +70,8 @@ int moe_permute_backward(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t 
   const int r = check_rows(T, K, rows, d, dtype);
   if (r != MOE_OK) return r;
   if (T == 0) return MOE_OK;
-  if (!dxs || !slot_row || !dx || lddxs < d || lddx < d || (base && ldbase < d)) return MOE_ERR_INVALID_ARG;
+  if ((rows > 0 && !dxs) || !slot_row || !dx || lddxs < d || lddx < d || (base && ldbase < d))
+    return MOE_ERR_INVALID_ARG;
   return launch_collect(T, K, rows, d, dtype, dxs, lddxs, nullptr, slot_row, base, ldbase, dx, lddx,
                         status_word(status), S(stream));
 }
@@ -80,7 +82,8 @@ int moe_unpermute(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype, 
   const int r = check_rows(T, K, rows, d, dtype);
   if (r != MOE_OK) return r;
   if (T == 0) return MOE_OK;
-  if (!ys || !weights || !slot_row || !y || ldys < d || ldy < d || (base && ldbase < d)) return MOE_ERR_INVALID_ARG;
+  if ((rows > 0 && !ys) || !weights || !slot_row || !y || ldys < d || ldy < d || (base && ldbase < d))
+    return MOE_ERR_INVALID_ARG;
   return launch_collect(T, K, rows, d, dtype, ys, ldys, weights, slot_row, base, ldbase, y, ldy, status_word(status),
                         S(stream));
 }
@@ -91,8 +94,9 @@ int moe_unpermute_backward(int32_t T, int32_t K, int64_t rows, int32_t d, int32_
   const int r = check_rows(T, K, rows, d, dtype);
   if (r != MOE_OK) return r;
   if (T == 0) return MOE_OK;
-  if (!dy || !weights || !slot_row || lddy < d || (!dys && !dweights)) return MOE_ERR_INVALID_ARG;
-  if ((dys && lddys < d) || ((ys != nullptr) != (dweights != nullptr)) || (ys && ldys < d)) return MOE_ERR_INVALID_ARG;
+  if (!dy || !weights || !slot_row || lddy < d || (dys && lddys < d) || (ys && ldys < d)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && ((!dys && !dweights) || ((ys != nullptr) != (dweights != nullptr)))) return MOE_ERR_INVALID_ARG;
+  if (rows == 0 && !dweights && !status) return MOE_OK;
   return launch_spread(T, K, rows, d, dtype, dy, lddy, ys, ldys, nullptr, weights, slot_row, dys, lddys, dweights,
                        status_word(status), S(stream));
 }
@@ -103,7 +107,8 @@ int moe_unpermute_backward8(int32_t T, int32_t K, int64_t rows, int32_t d, int32
   const int r = check_rows(T, K, rows, d, dtype);
   if (r != MOE_OK) return r;
   if (T == 0) return MOE_OK;
-  if (!dy || !codes || !scales || !weights || !slot_row || !dweights || lddy < d || (dys && lddys < d))
+  if (!dy || (rows > 0 && (!codes || !scales)) || !weights || !slot_row || !dweights || lddy < d ||
+      (dys && lddys < d))
     return MOE_ERR_INVALID_ARG;
   return launch_spread(T, K, rows, d, dtype, dy, lddy, codes, d, scales, weights, slot_row, dys, lddys, dweights,
                        status_word(status), S(stream));
