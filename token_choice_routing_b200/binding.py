@@ -459,18 +459,32 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype, dev: int):
-    """(data pointer, row stride) of a [rows, cols] row tensor."""
-    if t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == dev:
+def _rows(t: torch.Tensor, name: str, rows: Optional[int], cols: Optional[int], dtype: Optional[torch.dtype],
+          dev: int):
+    """(rows, columns, data pointer, row stride) of a row tensor; None in rows, cols or dtype: any."""
+    shape = t.shape
+    if (len(shape) == 2 and (rows is None or shape[0] == rows) and (cols is None or shape[1] == cols) and
+            (dtype is None or t.dtype is dtype) and t.get_device() == dev):
         ld, inner = t.stride()
-        if inner == 1 and ld >= cols:
-            return t.data_ptr(), ld
-    _placed(t, name, (rows, cols), dtype, dev)
-    if inner != 1 and cols > 1:
+        if inner == 1 and ld >= shape[1]:
+            return shape[0], shape[1], t.data_ptr(), ld
+    _two_d(t, name)
+    want = (shape[0] if rows is None else rows, shape[1] if cols is None else cols)
+    _placed(t, name, want, t.dtype if dtype is None else dtype, dev)
+    if inner != 1 and shape[1] > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    if ld < cols and rows > 1:
+    if ld < shape[1] and shape[0] > 1:
         raise ValueError(f"rows of {name} must not overlap")
-    return t.data_ptr(), max(ld, cols)
+    return shape[0], shape[1], t.data_ptr(), max(ld, shape[1])
+
+
+def _slots(t: torch.Tensor, T: int, dev: int):
+    """(K, data pointer) of slot_row [T, K]."""
+    shape = t.shape
+    if len(shape) == 2 and shape[0] == T and t.dtype is torch.int32 and t.get_device() == dev and t.is_contiguous():
+        return shape[1], t.data_ptr()
+    _two_d(t, "slot_row")
+    return shape[1], _dense(t, "slot_row", (T, shape[1]), torch.int32, dev)
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype: torch.dtype, dev: int) -> int:
@@ -496,7 +510,7 @@ def _device() -> int:
 
 def _raw_stream(stream, dev: int) -> int:
     """The stream's handle, without building a stream object for the current one (3 us a call,
-    a quarter of a decode-sized call's host time)."""
+    a third of a decode-sized call's host time)."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -512,9 +526,10 @@ def _status(ws: Optional[torch.Tensor], dev: int):
 
 
 def _two_d(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, not {len(shape)}")
+    return shape
 
 
 def sort_workspace_bytes(T: int, K: int, N: int) -> int:
@@ -537,94 +552,79 @@ def sort_slots(ids, N, counts, offsets, perm_tok, slot_row, ws, stream=None):
            LIB.moe_sort_slots(T, K, N, _dense(ids, "ids", (T, K), ids.dtype, dev), ids.element_size(),
                               _dense(counts, "counts", (N,), i32, dev), _dense(offsets, "offsets", (N + 1,), i32, dev),
                               _dense(perm_tok, "perm_tok", (T * K,), i32, dev),
-                              _dense(slot_row, "slot_row", (T, K), i32, dev), _status(ws, dev), _raw_stream(stream, dev)))
+                              _dense(slot_row, "slot_row", (T, K), i32, dev), _status(ws, dev),
+                              _raw_stream(stream, dev)))
 
 
 def permute(x, slot_row, xs, ws=None, stream=None):
     """xs[slot_row[t, k]] = x[t] for every slot with a row; the other rows of xs stay as they are."""
-    T, d = _two_d(x, "x")
-    K = _two_d(slot_row, "slot_row")[1]
-    rows = _two_d(xs, "xs")[0]
-    dev = _device()
-    dt = _dtype(x, "x")
-    px, ldx = _rows(x, "x", T, d, x.dtype, dev)
-    po, ldo = _rows(xs, "xs", rows, d, x.dtype, dev)
-    _check("moe_permute", LIB.moe_permute(T, K, rows, d, dt, px, ldx,
-                                          _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
-                                          _status(ws, dev), _raw_stream(stream, dev)))
+    dev, dt = _device(), _dtype(x, "x")
+    T, d, px, ldx = _rows(x, "x", None, None, None, dev)
+    K, ps = _slots(slot_row, T, dev)
+    rows, _, po, ldo = _rows(xs, "xs", None, d, x.dtype, dev)
+    _check("moe_permute", LIB.moe_permute(T, K, rows, d, dt, px, ldx, ps, po, ldo, _status(ws, dev),
+                                          _raw_stream(stream, dev)))
 
 
 def permute_backward(dxs, slot_row, dx, base=None, ws=None, stream=None):
     """dx[t] = base[t] + sum_k dxs[slot_row[t, k]]; base None is zero, base may be dx itself."""
-    T, d = _two_d(dx, "dx")
-    K = _two_d(slot_row, "slot_row")[1]
-    rows = _two_d(dxs, "dxs")[0]
-    dev = _device()
-    dt = _dtype(dx, "dx")
-    pi, ldi = _rows(dxs, "dxs", rows, d, dx.dtype, dev)
-    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, dx.dtype, dev)
-    po, ldo = _rows(dx, "dx", T, d, dx.dtype, dev)
+    dev, dt = _device(), _dtype(dx, "dx")
+    T, d, po, ldo = _rows(dx, "dx", None, None, None, dev)
+    K, ps = _slots(slot_row, T, dev)
+    rows, _, pi, ldi = _rows(dxs, "dxs", None, d, dx.dtype, dev)
+    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, dx.dtype, dev)[2:]
     _check("moe_permute_backward",
-           LIB.moe_permute_backward(T, K, rows, d, dt, pi, ldi,
-                                    _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
-                                    _status(ws, dev), _raw_stream(stream, dev)))
+           LIB.moe_permute_backward(T, K, rows, d, dt, pi, ldi, ps, pb, ldb, po, ldo, _status(ws, dev),
+                                    _raw_stream(stream, dev)))
 
 
 def unpermute(ys, weights, slot_row, y, base=None, ws=None, stream=None):
     """y[t] = base[t] + sum_k weights[t, k] ys[slot_row[t, k]]; base None is zero, base may be y
     itself."""
-    T, d = _two_d(y, "y")
-    K = _two_d(slot_row, "slot_row")[1]
-    rows = _two_d(ys, "ys")[0]
-    dev = _device()
-    dt = _dtype(y, "y")
-    pi, ldi = _rows(ys, "ys", rows, d, y.dtype, dev)
-    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, y.dtype, dev)
-    po, ldo = _rows(y, "y", T, d, y.dtype, dev)
+    dev, dt = _device(), _dtype(y, "y")
+    T, d, po, ldo = _rows(y, "y", None, None, None, dev)
+    K, ps = _slots(slot_row, T, dev)
+    rows, _, pi, ldi = _rows(ys, "ys", None, d, y.dtype, dev)
+    pb, ldb = (None, 0) if base is None else _rows(base, "base", T, d, y.dtype, dev)[2:]
     _check("moe_unpermute",
-           LIB.moe_unpermute(T, K, rows, d, dt, pi, ldi, _dense(weights, "weights", (T, K), torch.float32, dev),
-                             _dense(slot_row, "slot_row", (T, K), torch.int32, dev), pb, ldb, po, ldo,
-                             _status(ws, dev), _raw_stream(stream, dev)))
+           LIB.moe_unpermute(T, K, rows, d, dt, pi, ldi, _dense(weights, "weights", (T, K), torch.float32, dev), ps,
+                             pb, ldb, po, ldo, _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def unpermute_backward(dy, ys, weights, slot_row, dys, dweights, ws=None, stream=None):
     """dys[slot_row[t, k]] = weights[t, k] dy[t] and dweights[t, k] = <dy[t], ys[slot_row[t, k]]>
     (fp32 [T, K]). dys may be None, or ys and dweights both."""
-    T, d = _two_d(dy, "dy")
-    K = _two_d(slot_row, "slot_row")[1]
     if dys is None and ys is None:
         raise ValueError("dys and ys cannot both be None")
     if (ys is None) != (dweights is None):
         raise ValueError("ys and dweights go together")
-    rows = _two_d(ys if dys is None else dys, "ys" if dys is None else "dys")[0]
-    dev = _device()
-    dt = _dtype(dy, "dy")
+    dev, dt = _device(), _dtype(dy, "dy")
     f32 = torch.float32
-    pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
-    pi, ldi = (None, 0) if ys is None else _rows(ys, "ys", rows, d, dy.dtype, dev)
-    po, ldo = (None, 0) if dys is None else _rows(dys, "dys", rows, d, dy.dtype, dev)
+    T, d, pt, ldt = _rows(dy, "dy", None, None, None, dev)
+    K, ps = _slots(slot_row, T, dev)
+    rows, pi, ldi, po, ldo, pw = None, None, 0, None, 0, None
+    if ys is not None:
+        rows, _, pi, ldi = _rows(ys, "ys", None, d, dy.dtype, dev)
+        pw = _dense(dweights, "dweights", (T, K), f32, dev)
+    if dys is not None:
+        rows, _, po, ldo = _rows(dys, "dys", rows, d, dy.dtype, dev)
     _check("moe_unpermute_backward",
            LIB.moe_unpermute_backward(T, K, rows, d, dt, pt, ldt, pi, ldi, _dense(weights, "weights", (T, K), f32, dev),
-                                      _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
-                                      None if dweights is None else _dense(dweights, "dweights", (T, K), f32, dev),
-                                      _status(ws, dev), _raw_stream(stream, dev)))
+                                      ps, po, ldo, pw, _status(ws, dev), _raw_stream(stream, dev)))
 
 
 def unpermute_backward8(dy, codes, scales, weights, slot_row, dys, dweights, ws=None, stream=None):
     """``unpermute_backward`` with ys as ``checkpoint8`` stored it. dys may be None."""
-    T, d = _two_d(dy, "dy")
-    K = _two_d(slot_row, "slot_row")[1]
-    rows = _two_d(codes, "codes")[0]
-    dev = _device()
-    dt = _dtype(dy, "dy")
+    dev, dt = _device(), _dtype(dy, "dy")
     f32 = torch.float32
-    pt, ldt = _rows(dy, "dy", T, d, dy.dtype, dev)
-    po, ldo = (None, 0) if dys is None else _rows(dys, "dys", rows, d, dy.dtype, dev)
+    T, d, pt, ldt = _rows(dy, "dy", None, None, None, dev)
+    K, ps = _slots(slot_row, T, dev)
+    rows = _two_d(codes, "codes")[0]
+    po, ldo = (None, 0) if dys is None else _rows(dys, "dys", rows, d, dy.dtype, dev)[2:]
     _check("moe_unpermute_backward8",
            LIB.moe_unpermute_backward8(T, K, rows, d, dt, pt, ldt, _dense(codes, "codes", (rows, d), torch.int8, dev),
                                        _dense(scales, "scales", (rows, (d + 31) // 32), torch.uint8, dev),
-                                       _dense(weights, "weights", (T, K), f32, dev),
-                                       _dense(slot_row, "slot_row", (T, K), torch.int32, dev), po, ldo,
+                                       _dense(weights, "weights", (T, K), f32, dev), ps, po, ldo,
                                        _dense(dweights, "dweights", (T, K), f32, dev), _status(ws, dev),
                                        _raw_stream(stream, dev)))
 
@@ -638,16 +638,14 @@ def _used(rows_used, dev: int):
         return None
     if rows_used.numel() != 1:
         raise ValueError("rows_used must be one int32")
-    return _dense(rows_used, "rows_used", tuple(rows_used.shape), torch.int32, dev)
+    return _dense(rows_used, "rows_used", rows_used.shape, torch.int32, dev)
 
 
 def checkpoint8(x, codes, scales, rows_used=None, ws=None, stream=None):
     """x [rows, cols] stored in 8 bits: codes [rows, cols] int8, scales [rows, ceil(cols / 32)]
     uint8. rows_used (one int32 on the device, e.g. ``offsets[N:]``): the rows in use."""
-    rows, cols = _two_d(x, "x")
-    dev = _device()
-    dt = _dtype(x, "x")
-    px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
+    dev, dt = _device(), _dtype(x, "x")
+    rows, cols, px, ldx = _rows(x, "x", None, None, None, dev)
     _check("moe_checkpoint8",
            LIB.moe_checkpoint8(rows, cols, dt, px, ldx, _used(rows_used, dev),
                                _dense(codes, "codes", (rows, cols), torch.int8, dev),
@@ -657,10 +655,8 @@ def checkpoint8(x, codes, scales, rows_used=None, ws=None, stream=None):
 
 def restore8(codes, scales, x, rows_used=None, ws=None, stream=None):
     """The activation that ``checkpoint8`` stored, into x [rows, cols]."""
-    rows, cols = _two_d(x, "x")
-    dev = _device()
-    dt = _dtype(x, "x")
-    px, ldx = _rows(x, "x", rows, cols, x.dtype, dev)
+    dev, dt = _device(), _dtype(x, "x")
+    rows, cols, px, ldx = _rows(x, "x", None, None, None, dev)
     _check("moe_restore8",
            LIB.moe_restore8(rows, cols, dt, _dense(codes, "codes", (rows, cols), torch.int8, dev),
                             _dense(scales, "scales", (rows, (cols + 31) // 32), torch.uint8, dev),
@@ -672,12 +668,10 @@ def swiglu_backward8(codes, scales, dh, dz, h, packed=True, rows_used=None, ws=N
     [rows, 2F] from dh [rows, F], and the activation h [rows, F] recomputed (None: not written).
     packed: columns in the layer's order (64-column panels of gate, then up), else F gate
     columns, then F up columns."""
-    rows, F = _two_d(dh, "dh")
-    dev = _device()
-    dt = _dtype(dh, "dh")
-    pg, ldg = _rows(dh, "dh", rows, F, dh.dtype, dev)
-    pz, ldz = _rows(dz, "dz", rows, 2 * F, dh.dtype, dev)
-    ph, ldh = (None, 0) if h is None else _rows(h, "h", rows, F, dh.dtype, dev)
+    dev, dt = _device(), _dtype(dh, "dh")
+    rows, F, pg, ldg = _rows(dh, "dh", None, None, None, dev)
+    _, _, pz, ldz = _rows(dz, "dz", rows, 2 * F, dh.dtype, dev)
+    ph, ldh = (None, 0) if h is None else _rows(h, "h", rows, F, dh.dtype, dev)[2:]
     _check("moe_swiglu_backward8",
            LIB.moe_swiglu_backward8(rows, F, 1 if packed else 0, dt,
                                     _dense(codes, "codes", (rows, 2 * F), torch.int8, dev),

@@ -196,22 +196,44 @@ __global__ void __launch_bounds__(kCkptThreads, 2) checkpoint8_kernel(Ckpt8Args 
   }
 }
 
-// Rows of any width and alignment: a warp takes kElemBlocks consecutive blocks of one row (an
-// item), a lane one element of each, so that all addresses are one base plus constants. What is
-// the same for a whole block (its scale) is computed by one lane and handed round: the kernel is
-// bound by integer instructions (37 a block before that, at 77% of the ALU pipe: 93 us for
-// 60000 x 1001 in bf16).
+// Rows of any width and alignment: a warp takes kElemBlocks blocks (an item), a lane one element of
+// each: NB = 8 consecutive ones of a row, or of rows with fewer the NB (1, 2 or 4) of each of
+// 8 / NB consecutive rows, so that all addresses are one base plus constants. What is the same for
+// a whole block (its scale) is computed by one lane and handed round: the kernel is bound by integer
+// instructions (37 a block before that, at 77% of the ALU pipe: 93 us for 60000 x 1001 in bf16).
 constexpr int kElemBlocks = 8;
-constexpr int kElemCols = 32 * kElemBlocks;
 constexpr int kCkptWarps = kCkptThreads / 32;
 
-// One item; FULL: all its columns are in the row.
-template <typename E, bool FULL>
-__device__ __forceinline__ void store_item(const E* x, int8_t* codes, uint8_t* scales, int left, int blocks) {
+// An item's place: its first row and column, the rows and columns that are left from there.
+struct ElemSpot {
+  long long row;
+  int c0, rows, cols;
+  template <int NB>
+  __device__ __forceinline__ bool has(int u, int lane) const {  // block u has an element for this lane
+    return (NB == kElemBlocks || u / NB < rows) && (u % NB) * 32 + lane < cols;
+  }
+};
+template <int NB>
+__device__ __forceinline__ ElemSpot elem_spot(const Ckpt8Args& a, const ItemPos& p, long long used) {
+  constexpr int kRows = kElemBlocks / NB;
+  ElemSpot s;
+  s.row = p.row * kRows;
+  s.c0 = (int)p.i * (32 * NB);
+  s.rows = (int)min((long long)kRows, used - s.row);
+  s.cols = a.cols - s.c0;
+  return s;
+}
+
+// One item; FULL: all its elements are there.
+template <typename E, int NB, bool FULL>
+__device__ __forceinline__ void store_item(const Ckpt8Args& a, const ElemSpot& s) {
   const int lane = threadIdx.x & 31;
+  const E* x = static_cast<const E*>(a.x) + s.row * a.ld + s.c0 + lane;
+  int8_t* codes = a.codes + s.row * a.cols + s.c0 + lane;
   float v[kElemBlocks];
 #pragma unroll
-  for (int u = 0; u < kElemBlocks; ++u) v[u] = FULL || 32 * u < left ? elem_to_float<E>(__ldg(x + 32 * u)) : 0.f;
+  for (int u = 0; u < kElemBlocks; ++u)
+    v[u] = FULL || s.has<NB>(u, lane) ? elem_to_float<E>(__ldg(x + (u / NB) * a.ld + (u % NB) * 32)) : 0.f;
   uint32_t top = 0;  // lane u: of block u
 #pragma unroll
   for (int u = 0; u < kElemBlocks; ++u) {
@@ -224,29 +246,49 @@ __device__ __forceinline__ void store_item(const E* x, int8_t* codes, uint8_t* s
 #pragma unroll
   for (int u = 0; u < kElemBlocks; ++u) {
     const uint32_t q = clamp2(quantise(v[u], __shfl_sync(0xffffffffu, inv, u)));
-    if (FULL || 32 * u < left) codes[32 * u] = (int8_t)(((bad >> u) & 1u) ? 0u : q);
+    if (FULL || s.has<NB>(u, lane))
+      codes[(u / NB) * a.cols + (u % NB) * 32] = (int8_t)(((bad >> u) & 1u) ? 0u : q);
   }
-  if (lane < blocks) scales[lane] = (uint8_t)byte;
+  if (lane < kElemBlocks && s.has<NB>(lane, 0))
+    a.scales[(s.row + lane / NB) * a.nb + s.c0 / 32 + lane % NB] = (uint8_t)byte;
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads) checkpoint8_elem_kernel(Ckpt8Args a) {
-  pdl_wait_then_release();
+template <typename E, int NB, bool FULL>
+__device__ __forceinline__ void restore_item(const Ckpt8Args& a, const ElemSpot& s) {
   const int lane = threadIdx.x & 31;
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
+  E* x = static_cast<E*>(a.out) + s.row * a.ld + s.c0 + lane;
+  const int8_t* codes = a.codes + s.row * a.cols + s.c0 + lane;
+  int q[kElemBlocks];
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u)
+    q[u] = FULL || s.has<NB>(u, lane) ? (int)__ldg(codes + (u / NB) * a.cols + (u % NB) * 32) : 0;
+  const bool mine = lane < kElemBlocks && s.has<NB>(lane, 0);
+  const float sc =
+      scale_value(mine ? (uint32_t)__ldg(a.scales + (s.row + lane / NB) * a.nb + s.c0 / 32 + lane % NB) : 0u);
+#pragma unroll
+  for (int u = 0; u < kElemBlocks; ++u) {
+    const float v = (float)q[u] * __shfl_sync(0xffffffffu, sc, u);
+    if (FULL || s.has<NB>(u, lane)) x[(u / NB) * a.ld + (u % NB) * 32] = float_to_elem<E>(v);
+  }
+}
+
+template <typename E, int NB, bool STORE>
+__global__ void __launch_bounds__(kCkptThreads) ckpt8_elem_kernel(Ckpt8Args a) {
+  pdl_wait_then_release();
+  constexpr int kRows = kElemBlocks / NB;
+  const long long used = rows_in_use(a.used, a.rows, a.status);
+  const long long n = (used + kRows - 1) / kRows * a.walk.per_row.d;
   ItemPos p = at(a.walk.begin(), threadIdx.x >> 5, a.walk.per_row);  // this warp's item
   for (long long i = (long long)blockIdx.x * kCkptWarps + (threadIdx.x >> 5); i < n;
        i += (long long)gridDim.x * kCkptWarps, a.walk.next(p)) {
-    const int c0 = (int)p.i * kElemCols;
-    const int left = a.cols - c0 - lane;  // this lane's element of block u is in the row if 32 u < left
-    const E* x = static_cast<const E*>(a.x) + p.row * a.ld + c0 + lane;
-    int8_t* codes = a.codes + p.row * a.cols + c0 + lane;
-    uint8_t* scales = a.scales + p.row * a.nb + p.i * kElemBlocks;
-    const int blocks = min(kElemBlocks, a.nb - (int)p.i * kElemBlocks);
-    if (a.cols - c0 >= kElemCols)
-      store_item<E, true>(x, codes, scales, left, blocks);
-    else
-      store_item<E, false>(x, codes, scales, left, blocks);
+    const ElemSpot s = elem_spot<NB>(a, p, used);
+    if (s.rows == kRows && s.cols >= 32 * NB) {
+      if (STORE) store_item<E, NB, true>(a, s);
+      else restore_item<E, NB, true>(a, s);
+    } else {
+      if (STORE) store_item<E, NB, false>(a, s);
+      else restore_item<E, NB, false>(a, s);
+    }
   }
 }
 
@@ -291,41 +333,6 @@ __global__ void __launch_bounds__(kCkptThreads) restore8_kernel(Ckpt8Args a) {
       o.set(v);
       o.store(static_cast<E*>(a.out) + p.x);
     }
-  }
-}
-
-template <typename E, bool FULL>
-__device__ __forceinline__ void restore_item(const int8_t* codes, const uint8_t* scales, E* x, int left, int blocks) {
-  const int lane = threadIdx.x & 31;
-  int q[kElemBlocks];
-#pragma unroll
-  for (int u = 0; u < kElemBlocks; ++u) q[u] = FULL || 32 * u < left ? (int)__ldg(codes + 32 * u) : 0;
-  const float sc = scale_value(lane < blocks ? (uint32_t)__ldg(scales + lane) : 0u);
-#pragma unroll
-  for (int u = 0; u < kElemBlocks; ++u) {
-    const float v = (float)q[u] * __shfl_sync(0xffffffffu, sc, u);
-    if (FULL || 32 * u < left) x[32 * u] = float_to_elem<E>(v);
-  }
-}
-
-template <typename E>
-__global__ void __launch_bounds__(kCkptThreads) restore8_elem_kernel(Ckpt8Args a) {
-  pdl_wait_then_release();
-  const int lane = threadIdx.x & 31;
-  const long long n = rows_in_use(a.used, a.rows, a.status) * a.walk.per_row.d;
-  ItemPos p = at(a.walk.begin(), threadIdx.x >> 5, a.walk.per_row);
-  for (long long i = (long long)blockIdx.x * kCkptWarps + (threadIdx.x >> 5); i < n;
-       i += (long long)gridDim.x * kCkptWarps, a.walk.next(p)) {
-    const int c0 = (int)p.i * kElemCols;
-    const int left = a.cols - c0 - lane;
-    E* x = static_cast<E*>(a.out) + p.row * a.ld + c0 + lane;
-    const int8_t* codes = a.codes + p.row * a.cols + c0 + lane;
-    const uint8_t* scales = a.scales + p.row * a.nb + p.i * kElemBlocks;
-    const int blocks = min(kElemBlocks, a.nb - (int)p.i * kElemBlocks);
-    if (a.cols - c0 >= kElemCols)
-      restore_item<E, true>(codes, scales, x, left, blocks);
-    else
-      restore_item<E, false>(codes, scales, x, left, blocks);
   }
 }
 
@@ -538,25 +545,40 @@ static bool ckpt8_vec(const Ckpt8Args& a, const void* x, int bytes, bool* flat) 
   return a.cols % 8 == 0 && rows_aligned16(x, a.ld, bytes) && codes % 8 == 0;
 }
 
+template <typename E, int NB, bool STORE>
+static int ckpt8_elem_go(Ckpt8Args a, cudaStream_t st) {
+  constexpr int kRows = kElemBlocks / NB;
+  unsigned grid;
+  a.walk = make_walk((a.rows + kRows - 1) / kRows, (a.nb + NB - 1) / NB, kCkptWarps, kCkptCtas, &grid);
+  return launch_pdl(ckpt8_elem_kernel<E, NB, STORE>, dim3(grid), dim3(kCkptThreads), 0, st, a);
+}
+
+template <typename E, bool STORE>
+static int ckpt8_elem_run(const Ckpt8Args& a, cudaStream_t st) {
+  // several rows an item while a row has at most half the blocks of one (262144 x 7, store and
+  // restore: 30 us, 128 with one row an item)
+  if (a.nb == 1) return ckpt8_elem_go<E, 1, STORE>(a, st);
+  if (a.nb == 2) return ckpt8_elem_go<E, 2, STORE>(a, st);
+  return a.nb <= 4 ? ckpt8_elem_go<E, 4, STORE>(a, st) : ckpt8_elem_go<E, 8, STORE>(a, st);
+}
+
 template <typename E>
 static int checkpoint8_run(Ckpt8Args a, cudaStream_t st) {
   bool flat;
-  const bool vec = ckpt8_vec(a, a.x, sizeof(E), &flat);
+  if (!ckpt8_vec(a, a.x, sizeof(E), &flat)) return ckpt8_elem_run<E, true>(a, st);
   unsigned grid;
-  a.walk = make_walk(a.rows, vec ? 2 * a.nb : (a.cols + kElemCols - 1) / kElemCols,
-                     vec ? kCkptThreads * kUnroll : kCkptWarps, kCkptCtas, &grid);
-  auto kern = !vec ? checkpoint8_elem_kernel<E> : flat ? checkpoint8_kernel<E, true> : checkpoint8_kernel<E, false>;
+  a.walk = make_walk(a.rows, 2 * a.nb, kCkptThreads * kUnroll, kCkptCtas, &grid);
+  auto kern = flat ? checkpoint8_kernel<E, true> : checkpoint8_kernel<E, false>;
   return launch_pdl(kern, dim3(grid), dim3(kCkptThreads), 0, st, a);
 }
 
 template <typename E>
 static int restore8_run(Ckpt8Args a, cudaStream_t st) {
   bool flat;
-  const bool vec = ckpt8_vec(a, a.out, sizeof(E), &flat);
+  if (!ckpt8_vec(a, a.out, sizeof(E), &flat)) return ckpt8_elem_run<E, false>(a, st);
   unsigned grid;
-  a.walk = make_walk(a.rows, vec ? a.cols * (int)sizeof(E) / 16 : (a.cols + kElemCols - 1) / kElemCols,
-                     vec ? kCkptThreads * kRestoreUnroll : kCkptWarps, kCkptCtas, &grid);
-  auto kern = !vec ? restore8_elem_kernel<E> : flat ? restore8_kernel<E, true> : restore8_kernel<E, false>;
+  a.walk = make_walk(a.rows, (long long)a.cols * sizeof(E) / 16, kCkptThreads * kRestoreUnroll, kCkptCtas, &grid);
+  auto kern = flat ? restore8_kernel<E, true> : restore8_kernel<E, false>;
   return launch_pdl(kern, dim3(grid), dim3(kCkptThreads), 0, st, a);
 }
 
