@@ -270,6 +270,19 @@ def test_a_block_stored_as_nan_reaches_the_gate_gradient():
     assert bool(torch.isnan(dw[0, 0])) and float(dw[1, 0]) == 64.0
 
 
+def test_large_gradients_against_small_scales_stay_finite():
+    """Products that are in range only with the block's scale applied first."""
+    for d in (64, 33):
+        dy = torch.full((2, d), 3e36, device="cuda")
+        codes = torch.full((2, d), 100, dtype=torch.int8, device="cuda")
+        scales = torch.full((2, (d + 31) // 32), 107, dtype=torch.uint8, device="cuda")      # 2^-20
+        sr = torch.tensor([[1], [0]], dtype=torch.int32, device="cuda")
+        dw = torch.zeros((2, 1), device="cuda")
+        B.unpermute_backward8(dy, codes, scales, torch.ones((2, 1), device="cuda"), sr, None, dw)
+        ref = f64(dy)[0].sum() * 100 * 2.0 ** -20
+        assert np.all(np.abs(f64(dw) - ref) <= (d + 2) * V * ref)
+
+
 def test_non_finite_rows_go_where_their_slots_do():
     for dt in TYPES.values():
         ys = torch.ones((4, 40), dtype=dt, device="cuda")

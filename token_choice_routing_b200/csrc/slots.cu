@@ -483,16 +483,17 @@ __global__ void __launch_bounds__(kRowThreads) spread_kernel(RowArgs a) {
   }
 }
 
-// The dot product of a piece with unscaled codes.
+// s + the dot product of a piece with codes of scale sc. The values code * sc are exact; scaling the
+// sum instead would save a multiplication an element (1 to 2% of the kernel) and overflow where
+// the scaled products do not.
 template <int V>
-__device__ __forceinline__ float dot_codes(const float (&g)[V], const CodePiece<V>& q) {
-  float s = 0.f;
+__device__ __forceinline__ float dot_codes(const float (&g)[V], const CodePiece<V>& q, float sc, float s) {
 #pragma unroll
   for (int j = 0; j < V; j += 4) {
     float f[4];
     codes_to_float(q.word[j / 4], f);
 #pragma unroll
-    for (int i = 0; i < (V < 4 ? V : 4); ++i) s = fmaf(g[j + i], f[i], s);
+    for (int i = 0; i < (V < 4 ? V : 4); ++i) s = fmaf(g[j + i], f[i] * sc, s);
   }
   return s;
 }
@@ -502,7 +503,7 @@ __device__ __forceinline__ float dot_codes(const float (&g)[V], const CodePiece<
 // wpt-th chunk of its columns. A dot product is summed in fp32 per lane, over the lanes by a fixed
 // shuffle tree and over the warps in order, so it does not depend on timing.
 // Bound by HBM: T = 65536, d = 2048, K = 8, half the slots null, bf16 375 us (6.5 TB/s), from codes
-// 315 us (6.0 TB/s); T = 16384 102 us; from codes at d = 1024, K = 4 29 us (4.7 TB/s), where a token
+// 319 us (6.0 TB/s); T = 16384 102 us; from codes at d = 1024, K = 4 29 us (4.7 TB/s), where a token
 // has two rows and a warp's chain of lookup, loads and stores is not covered. A persistent grid
 // that looks the next token's slots up ahead measured slower (375 -> 401 us and more).
 // Eight single elements of five rows a lane need more registers than four CTAs leave (T = 16384,
@@ -575,13 +576,11 @@ __global__ void __launch_bounds__(kRowThreads, V == 1 && NV == kElemPieces ? (CO
             float gf[V];
             g[v].get(gf);
             if constexpr (CODES && V == 1)  // before any lane leaves; columns past the row hold zeros
-              dot[u] = fmaf(gf[0] * (float)(int)q[u][v].word[0], __shfl_sync(0xffffffffu, lane_scale, u * NV + v),
-                            dot[u]);
+              dot[u] = fmaf(gf[0], (float)(int)q[u][v].word[0] * __shfl_sync(0xffffffffu, lane_scale, u * NV + v), dot[u]);
             if (c >= a.d) continue;
             if constexpr (CODES && V == 1) {
             } else if constexpr (CODES) {
-              // the sum over a piece, then its scale: a power of two, exact
-              dot[u] = fmaf(dot_codes<V>(gf, q[u][v]), scale_value(sb[u][v]), dot[u]);
+              dot[u] = dot_codes<V>(gf, q[u][v], scale_value(sb[u][v]), dot[u]);
             } else {
               float pf[V];
               p[u][v].get(pf);
@@ -719,7 +718,7 @@ __global__ void __launch_bounds__(kRowThreads) spread_dot_narrow_kernel(RowArgs 
       if constexpr (CODES) {
         const CodePiece<V> q = load_codes<V>(static_cast<const int8_t*>(a.rows_in) + at);
         const float sc = scale_value(__ldg(a.scales + (long long)r[u] * nb + (c >> 5)));
-        dot[u] = dot_codes<V>(gf, q) * sc;
+        dot[u] = dot_codes<V>(gf, q, sc, 0.f);
       } else {
         Piece<E, V> p;
         p.load(static_cast<const E*>(a.rows_in) + at);
