@@ -21,22 +21,23 @@ namespace moe {
 // chunks below its own and writes the rows. Integer sums only, so the result is exact whatever the
 // order. With one chunk the placing kernel does it alone.
 //
-// What bounds it is instructions and the chain of dependent steps, not the 12 bytes a slot. So the
-// ids are read once and stay in registers with their ranks, and with two kernels the ranking runs
-// before the wait for the first one's table (the ids were complete before that kernel let this one
-// start): 1M slots, 64 experts 14.1 us, of which the ranking and the launch are 6.6 us; 256 slots 3.0 us.
-// Ranks written by a first kernel and only offset by a second one took 14.3 us, and 10.2 against 7.1
-// at 256k slots. A warp takes 32 slots at a time; lanes of the same id find each other by one ballot per
-// bit of the ids (a match instruction, which goes value by value, took 13 against 5 us for 16384
-// slots; counters of a byte per lane and expert, summed by multiplication, took the same time as
-// the ballots at 1M slots and more at fewer).
+// What bounds it is the chain of dependent steps, not the 12 bytes a slot. So the ids are read once
+// and stay in registers with their ranks, and with two kernels the ranking runs before the wait for
+// the first one's table (the ids were complete before that kernel let this one start). 64 experts:
+// 256 slots 2.8 us, 16k 4.9, 256k 6.8, 1M 12.8; in the last the counting takes 2.0 us, the ranking 2.8,
+// the table's sums 1.8 and the rows, 4-byte stores all over perm_tok, 2.3 to 3.6. Ranks written by a
+// first kernel and only offset by a second one took 14.3 us, and 10.2 at 256k slots.
+// A warp takes 32 slots at a time; lanes of the same id find each other by one ballot per bit of the
+// ids (a match instruction, which goes value by value, took 13 against 5 us for 16k slots; counters of
+// a byte per lane and expert, summed by multiplication, were no faster at 1M slots and slower at fewer).
 constexpr int kSortItems = 8;  // slots a thread holds; a CTA ranks 256 a warp at a time
+constexpr int kCountThreads = 512;
 constexpr int kSortMaxChunks = 148;
 // One CTA does up to kSortOneChunk slots alone; more are cut into chunks of 1024 slots, or more once
 // there are kSortMaxChunks of them (64 experts: 8192 slots 4.7 us; in chunks of 4096 10.2 us).
 constexpr int kSortOneChunk = 2048;
 // 16 warps a CTA while they rank a chunk in one pass, 32 beyond (a single step of 256 slots 3.0 us
-// against 3.7 with 32 warps; 1M slots, 512 experts 28.9 against 42.7 with 16).
+// against 3.7 with 32 warps; 1M slots, 512 experts 28 against 43 with 16).
 constexpr int kSortFewWarps = 4096;
 
 struct SortShape {
@@ -82,9 +83,9 @@ __device__ __forceinline__ int sort_id(const SortArgs& a, long long s, long long
   return (v >= 0 && v < (Id)a.N) ? (int)v : -1;
 }
 
-template <typename Id, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) sort_count_kernel(SortArgs a) {
-  constexpr int kThreads = WARPS * 32, kPass = kThreads * kSortItems;
+template <typename Id>
+__global__ void __launch_bounds__(kCountThreads) sort_count_kernel(SortArgs a) {
+  constexpr int kThreads = kCountThreads, kPass = kThreads * kSortItems;
   pdl_wait_then_release();
   extern __shared__ int s_mem[];
   int* hist = s_mem;
@@ -125,6 +126,7 @@ static size_t sort_smem(int N, int warps) { return sizeof(int) * ((size_t)warps 
 template <int WARPS>
 __device__ __forceinline__ void sort_first_rows(const SortArgs& a, const SortShared& m) {
   constexpr int kThreads = WARPS * 32;
+  constexpr int kBatch = 10;  // loads in flight: 148 rows of 64 experts by 1024 threads at once
   const int N = a.N, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (a.chunks > 1) {
     // column sums: a thread takes expert g in every (kThreads / width)-th row. Not the
@@ -132,11 +134,18 @@ __device__ __forceinline__ void sort_first_rows(const SortArgs& a, const SortSha
     const int width = min(kThreads, max(32, 1 << (32 - __clz(N - 1)))), rows = kThreads / width;
     for (int g = tid & (width - 1); g < N; g += width) {
       int all = 0, below = 0;
-#pragma unroll 8
-      for (int c = tid / width; c < a.chunks; c += rows) {
-        const int v = __ldcg(a.table + (size_t)c * N + g);
-        all += v;
-        below += c < (int)blockIdx.x ? v : 0;
+      for (int c0 = tid / width; c0 < a.chunks; c0 += rows * kBatch) {
+        int v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = c0 + i * rows;
+          v[i] = c < a.chunks ? __ldcg(a.table + (size_t)c * N + g) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          all += v[i];
+          below += c0 + i * rows < (int)blockIdx.x ? v[i] : 0;
+        }
       }
       atomicAdd(&m.base[g], all);
       atomicAdd(&m.pre[g], below);
@@ -227,8 +236,12 @@ __device__ __forceinline__ unsigned same_id(int id) {
   return peers;
 }
 
+// Its registers have to leave room for a CTA of the counting kernel (512 threads of 32), so that the
+// ranking starts while that one still runs: two CTAs' worth with 16 warps; 32 warps take 43 registers
+// as they are (bounded to 64 14.1 us at 1M slots, to 48 13.7, this 12.8; 16 warps unbounded 8.4 against
+// 6.8 us at 256k).
 template <typename Id, int WARPS, int BITS>
-__global__ void __launch_bounds__(WARPS * 32) sort_place_kernel(SortArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 2 : 0) sort_place_kernel(SortArgs a) {
   constexpr int kThreads = WARPS * 32, kPass = kThreads * kSortItems;
   extern __shared__ int s_mem[];
   const SortShared m(s_mem, a.N, WARPS);
@@ -282,7 +295,7 @@ static int sort_go(const SortArgs& a, cudaStream_t st) {
     return MOE_ERR_CUDA;
   const dim3 grid(a.chunks), block(WARPS * 32);
   if (a.chunks > 1) {
-    const int r = launch_pdl(sort_count_kernel<Id, WARPS>, grid, block, sizeof(int) * (size_t)a.N, st, a);
+    const int r = launch_pdl(sort_count_kernel<Id>, grid, dim3(kCountThreads), sizeof(int) * (size_t)a.N, st, a);
     if (r != MOE_OK) return r;
   }
   return launch_pdl(place, grid, block, smem, st, a);
