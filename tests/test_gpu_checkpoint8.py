@@ -249,6 +249,25 @@ def test_swiglu_backward8_extremes():
     assert bool((dz[3, :F] == 1.5).all()) and bool((dz[3, F:] == 0.0).all())
 
 
+@pytest.mark.parametrize("packed,F", [(True, 64), (False, 37)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_swiglu_backward8_large_products(dtype, packed, F):
+    """dh b passes fp32's range while a closed gate keeps the gradient finite."""
+    a = [-20, -60, -87, -100, -127, 0]
+    codes = torch.empty((len(a), 2 * F), dtype=torch.int8, device="cuda")
+    codes[:, :F] = torch.tensor(a, dtype=torch.int8, device="cuda")[:, None]
+    codes[:, F:] = 100
+    scales = torch.full((len(a), (2 * F + 31) // 32), 127, dtype=torch.uint8, device="cuda")
+    # up: 100 x 2^60; with 37 gate columns the block they share with the up columns keeps scale 1
+    scales[:, (F + 31) // 32:] = 187
+    dh = torch.full((len(a), F), 1e20, dtype=TYPES[dtype], device="cuda")
+    dh[-1] = 1.0
+    dz, h = torch.empty((len(a), 2 * F), dtype=TYPES[dtype], device="cuda"), torch.empty_like(dh)
+    B.swiglu_backward8(codes, scales, dh, dz, h, packed=packed)
+    assert bool(torch.isfinite(dz).all()) and bool(torch.isfinite(h).all())
+    check_swiglu(codes, scales, dh, dz, h, packed)
+
+
 def test_swiglu_backward8_agrees_with_differences():
     """dz against central differences of sum(h dh), h = silu(a) b, in 64 bits at the stored values."""
     rows, F, eps = 9, 96, 1e-4

@@ -351,7 +351,8 @@ struct Swiglu8Args {
 
 // da = dh b s (1 + a (1 - s)), db = dh a s, h = a s b with s = 1 / (1 + exp(-a)); fp32, one
 // rounding per output. expf is within 2 ulp and the approximate reciprocal within 1; it gives 0
-// where exp(-a) passes 2^126, as s is below fp32's normal range there.
+// where exp(-a) passes 2^126, as s is below fp32's normal range there. dh comes last in da: dh b
+// alone may overflow where a small s leaves the gradient finite.
 struct SwigluOut {
   float da, db, h;
 };
@@ -359,7 +360,7 @@ __device__ __forceinline__ SwigluOut swiglu_grad(float a, float b, float g) {
   float s;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + expf(-a)));
   const float as = a * s;
-  return {g * b * s * (1.f + a * (1.f - s)), g * as, as * b};
+  return {g * (b * (s * (1.f + a * (1.f - s)))), g * as, as * b};
 }
 
 // Rows of 16-byte pieces: an item is eight pairs. FLAT: dense rows in the packed order, where the
