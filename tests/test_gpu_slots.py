@@ -602,3 +602,42 @@ def test_routed_refusals_and_no_tokens():
     layer, x, _ = H.make_layer(I.make_inputs(pp))
     with pytest.raises(ValueError):
         layer.forward_routed(x, ids[:8], gate[:8])
+
+
+def test_results_of_a_passed_stream_outlive_their_scratch():
+    """Only y (and the gradients) of a call on a stream that has other work to do first are kept; the
+    current stream then takes and overwrites memory of the sizes that were dropped. With zeros:
+    a wrong index would be a valid one."""
+    from tests import gpu_helpers as H
+    cfg = ROUTED["wide"]
+    layer, x, _ = H.make_layer(I.make_inputs(cfg))
+    ids = draw_ids(np.random.default_rng(3), cfg.T, 3, cfg.N, 0.3)
+    gate = torch.rand((cfg.T, 3), device="cuda")
+    dy = torch.randn((cfg.T, cfg.d), device="cuda").to(torch.bfloat16)
+    out = layer.forward_routed(x, ids, gate)
+    want = dict(y=out["y"].clone(), own=layer.forward(x)["y"].clone())
+    want.update((n, t.clone()) for n, t in layer.backward_routed(x, gate, out, dy).items() if n.startswith("dw"))
+    busy = torch.ones((8192, 8192), device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+
+    def crowd():
+        for sizes in (layer.alloc_routed(cfg.T, 3), layer.alloc_routed_grads(cfg.T, 3), layer.alloc(cfg.T)):
+            for t in sizes.values():
+                if t is not None:
+                    t.zero_()
+
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy @ busy
+        got = dict(y=layer.forward_routed(x, ids, gate, stream=side)["y"], own=layer.forward(x, stream=side)["y"])
+        crowd()
+        g = layer.backward_routed(x, gate, out, dy, stream=side)
+        got.update((n, g[n]) for n in want if n.startswith("dw"))
+        del g
+        crowd()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for n, t in want.items():
+            assert torch.equal(got[n], t), n

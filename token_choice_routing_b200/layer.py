@@ -178,6 +178,22 @@ class MoENullLayer:
         out["workspace"] = torch.empty((max(B.workspace_bytes(self.dims(T)), 256),), dtype=torch.uint8, device=dev)
         return out
 
+    def _allocated(self, stream, make) -> Dict[str, torch.Tensor]:
+        """``make()``'s buffers for a call that runs on ``stream`` (None: the current one). They
+        belong to that stream, so that the memory of one that is dropped goes to nothing else
+        before the call is done with it. What the current stream does with them afterwards is
+        recorded in the same way."""
+        if stream is None:
+            return make()
+        cur = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            bufs = make()
+        if stream.cuda_stream != cur.cuda_stream:
+            for t in bufs.values():
+                if t is not None:
+                    t.record_stream(cur)
+        return bufs
+
     def alloc_grads(self, T: int, checkpoint8: bool = False) -> Dict[str, torch.Tensor]:
         """Gradient buffers and the backward workspace for a T-token backward
         (checkpoint8=True: for ``backward_checkpoint8``, whose workspace also holds the rows
@@ -224,7 +240,7 @@ class MoENullLayer:
         """Gradients of <y, dy> + alpha L_bal + beta L_z through ``moe_backward``."""
         T = x.shape[0]
         if grads is None:
-            grads = self.alloc_grads(T)
+            grads = self._allocated(stream, lambda: self.alloc_grads(T))
         sv = self.saved(x, out, counts_ext, t_total)
         g = B.Grads(*[None if grads.get(n) is None else grads[n].data_ptr() for n in B.GRAD_FIELDS])
         B.backward(self.dims(T), self._weights, sv, dy, alpha, beta, g, grads["workspace"], stream)
@@ -286,7 +302,7 @@ class MoENullLayer:
         if ck["slot_row"].shape[0] < T:
             raise ValueError(f"the checkpoint holds {ck['slot_row'].shape[0]} tokens, not {T}")
         if grads is None:
-            grads = self.alloc_grads(T, checkpoint8=True)
+            grads = self._allocated(stream, lambda: self.alloc_grads(T, checkpoint8=True))
         if grads["workspace"].numel() < B.backward_checkpoint8_workspace_bytes(dm):
             raise ValueError("grads must come from alloc_grads(T, checkpoint8=True)")
         sv = B.Saved8()
@@ -345,7 +361,7 @@ class MoENullLayer:
             raise B.MoEError("moe_check_dims", B.check_dims(dm))
         self._check_tokens("x", x, T)
         if out is None:
-            out = self.alloc_routed(T, K)
+            out = self._allocated(stream, lambda: self.alloc_routed(T, K))
         ws = out["workspace"]
         B.sort_slots(topk_idx, self.N, out["counts"], out["offsets"], out["perm_tok"], out["slot_row"], ws, stream)
         if T == 0:
@@ -391,7 +407,7 @@ class MoENullLayer:
         self._check_tokens("x", x, T)
         self._check_tokens("dy", dy, T)
         if grads is None:
-            grads = self.alloc_routed_grads(T, K)
+            grads = self._allocated(stream, lambda: self.alloc_routed_grads(T, K))
         if T == 0:
             return grads
         ws = grads["workspace"]
@@ -514,7 +530,7 @@ class MoENullLayer:
                 out: Optional[Dict[str, torch.Tensor]] = None, stream=None) -> Dict[str, torch.Tensor]:
         T = x.shape[0]
         if out is None:
-            out = self.alloc(T)
+            out = self._allocated(stream, lambda: self.alloc(T))
         o = B.Outputs(*[None if out.get(n) is None else out[n].data_ptr() for n in B.OUTPUT_FIELDS])
         B.forward(self.dims(T), self._weights, x, tok_null_bias, o, out["workspace"], stream)
         return out
