@@ -743,7 +743,8 @@ typedef struct moe_saved8 {
 MOE_API size_t moe_backward_checkpoint8_workspace_bytes(const moe_dims_t* dims);
 
 /* moe_backward from an 8-bit checkpoint: the same gradients of the layer at the stored
- * pre-activations and outputs. */
+ * pre-activations and outputs. As in moe_backward, T = 0 writes nothing: whoever sums weight
+ * gradients over ranks takes zeros from a rank without tokens. */
 MOE_API int moe_backward_checkpoint8(const moe_dims_t* dims, const moe_weights_t* w, const moe_saved8_t* saved,
                                      const uint16_t* dy, float alpha, float beta, const moe_grads_t* g,
                                      void* workspace, moe_stream_t stream);

@@ -467,3 +467,27 @@ def test_checkpoint_refusals():
         layer.backward_checkpoint8(x, layer.alloc_checkpoint8(cfg.T - 1), dy)
     with pytest.raises(ValueError):
         layer.backward_checkpoint8(x, ck, dy, grads=layer.alloc_grads(cfg.T))
+
+
+@pytest.mark.parametrize("name", ["ragged", "pp"])
+def test_a_checkpointed_backward_without_tokens_gives_zero_gradients(name):
+    """A rank without tokens adds zeros to the others' weight gradients, whatever the buffers held;
+    the gradients of the tokens, of which there are none, stay as they were."""
+    cfg = CASES[name]
+    layer, x, tnb = H.make_layer(I.make_inputs(cfg))
+    x, tnb = x[:0], None if tnb is None else tnb[:0]
+    ck, out = layer.alloc_checkpoint8(0), layer.alloc(0)
+    grads = layer.alloc_grads(0, checkpoint8=True)
+    for stream in (None, torch.cuda.Stream()):
+        for n in B.GRAD_FIELDS:
+            if grads[n] is not None:
+                grads[n].fill_(float("nan"))
+        torch.cuda.synchronize()
+        layer.forward_checkpoint8(x, tnb, out, ck, stream)
+        g = layer.backward_checkpoint8(x, ck, x, ALPHA, BETA, grads, torch.ones_like(ck["counts_ext"]), cfg.T, stream)
+        torch.cuda.synchronize()
+        for n in B.GRAD_FIELDS:
+            if n in ("dx", "dtok_null_bias"):
+                assert bool(torch.isnan(g[n]).all()), n
+            elif g[n] is not None:
+                assert int(torch.count_nonzero(g[n])) == 0, n

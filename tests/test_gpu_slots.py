@@ -641,3 +641,23 @@ def test_results_of_a_passed_stream_outlive_their_scratch():
         torch.cuda.synchronize()
         for n, t in want.items():
             assert torch.equal(got[n], t), n
+
+
+def test_a_routed_backward_without_tokens_gives_zero_gradients():
+    """A rank without tokens adds zeros to the others' weight gradients, whatever the buffers held."""
+    from tests import gpu_helpers as H
+    cfg = ROUTED["ragged"]
+    layer, x, _ = H.make_layer(I.make_inputs(cfg))
+    gate = torch.ones((0, 2), device="cuda")
+    out = layer.forward_routed(x[:0], torch.zeros((0, 2), dtype=torch.int32, device="cuda"), gate)
+    grads = layer.alloc_routed_grads(0, 2)
+    names = [n for n in B.GRAD_FIELDS if n in grads and n != "dx"]
+    for stream in (None, torch.cuda.Stream()):
+        for n in names:
+            grads[n].fill_(float("nan"))
+        torch.cuda.synchronize()
+        g = layer.backward_routed(x[:0], gate, out, x[:0], grads, stream=stream)
+        torch.cuda.synchronize()
+        for n in names:
+            assert int(torch.count_nonzero(g[n])) == 0, n
+    assert sorted(names) == ["dw_down", "dw_gate", "dw_up", "dws_down", "dws_gate", "dws_up"]

@@ -194,6 +194,15 @@ class MoENullLayer:
                     t.record_stream(cur)
         return bufs
 
+    @staticmethod
+    def _zero_weight_grads(grads: Dict[str, torch.Tensor], stream):
+        """The gradients of a call without tokens: sums over none. The library's calls write
+        nothing then, so the buffers would keep what the last step left in them."""
+        with torch.cuda.stream(stream):
+            for n in B.GRAD_FIELDS:
+                if n not in ("dx", "dtok_null_bias") and grads.get(n) is not None:
+                    grads[n].zero_()
+
     def alloc_grads(self, T: int, checkpoint8: bool = False) -> Dict[str, torch.Tensor]:
         """Gradient buffers and the backward workspace for a T-token backward
         (checkpoint8=True: for ``backward_checkpoint8``, whose workspace also holds the rows
@@ -237,7 +246,8 @@ class MoENullLayer:
                  beta: float = 1e-3, grads: Optional[Dict[str, torch.Tensor]] = None,
                  counts_ext: Optional[torch.Tensor] = None, t_total: Optional[int] = None,
                  stream=None) -> Dict[str, torch.Tensor]:
-        """Gradients of <y, dy> + alpha L_bal + beta L_z through ``moe_backward``."""
+        """Gradients of <y, dy> + alpha L_bal + beta L_z through ``moe_backward``, which without
+        tokens (T = 0) writes nothing."""
         T = x.shape[0]
         if grads is None:
             grads = self._allocated(stream, lambda: self.alloc_grads(T))
@@ -295,8 +305,8 @@ class MoENullLayer:
                              counts_ext: Optional[torch.Tensor] = None, t_total: Optional[int] = None,
                              stream=None) -> Dict[str, torch.Tensor]:
         """``backward`` from what ``forward_checkpoint8`` kept: the gradients at the stored
-        pre-activations and outputs (``moe_backward_checkpoint8``). grads: from
-        ``alloc_grads(T, checkpoint8=True)``."""
+        pre-activations and outputs (``moe_backward_checkpoint8``). Without tokens (T = 0) the
+        gradients of the weights are zeros. grads: from ``alloc_grads(T, checkpoint8=True)``."""
         T = x.shape[0]
         dm = self.dims(T)
         if ck["slot_row"].shape[0] < T:
@@ -313,6 +323,8 @@ class MoENullLayer:
         sv.t_total = int(T if t_total is None else t_total)
         g = B.Grads(*[None if grads.get(n) is None else grads[n].data_ptr() for n in B.GRAD_FIELDS])
         B.backward_checkpoint8(dm, self._weights, sv, dy, alpha, beta, g, grads["workspace"], stream)
+        if T == 0:
+            self._zero_weight_grads(grads, stream)
         return grads
 
     # ------------------------------------------------------- the experts on a given routing
@@ -401,7 +413,8 @@ class MoENullLayer:
                         stream=None) -> Dict[str, torch.Tensor]:
         """Gradients of <y, dy> after ``forward_routed``: dx, the experts' and the shared expert's
         weights, and dgate [T, K] for whatever computed the gates. The router has no part in it.
-        Buffers from ``alloc_routed_grads(T, K)``."""
+        Without tokens (T = 0) the gradients of the weights are zeros. Buffers from
+        ``alloc_routed_grads(T, K)``."""
         T, K = topk_gate.shape
         dm = self._routed_dims(T, K)
         self._check_tokens("x", x, T)
@@ -409,6 +422,7 @@ class MoENullLayer:
         if grads is None:
             grads = self._allocated(stream, lambda: self.alloc_routed_grads(T, K))
         if T == 0:
+            self._zero_weight_grads(grads, stream)
             return grads
         ws = grads["workspace"]
         ptr = lambda t: t.data_ptr()
