@@ -661,3 +661,36 @@ def test_a_routed_backward_without_tokens_gives_zero_gradients():
         for n in names:
             assert int(torch.count_nonzero(g[n])) == 0, n
     assert sorted(names) == ["dw_down", "dw_gate", "dw_up", "dws_down", "dws_gate", "dws_up"]
+
+
+def test_sorts_of_two_threads():
+    """Two host threads, whose calls need different amounts of shared memory of the same kernel."""
+    import threading
+    T, K = 1024, 4
+    failed = []
+
+    def work(N):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ids = draw_ids(np.random.default_rng(N), T, K, N, 0.2)
+                counts, offsets, _, row = sort_ref(ids.cpu().numpy(), N)
+                z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+                o = (z(N), z(N + 1), z(T * K), z(T, K))
+                ws = torch.empty(B.sort_workspace_bytes(T, K, N), dtype=torch.uint8, device="cuda")
+                for _ in range(8):
+                    o[3].zero_()
+                    for _ in range(1000):
+                        B.sort_slots(ids, N, *o, ws)
+                    assert np.array_equal(o[0].cpu().numpy(), counts) and np.array_equal(o[1].cpu().numpy(), offsets)
+                    assert np.array_equal(o[3].cpu().numpy(), row)
+        except Exception as e:  # noqa: BLE001  (the main thread reports it)
+            failed.append((N, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(N,)) for N in (700, 1024)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed

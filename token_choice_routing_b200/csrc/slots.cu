@@ -286,24 +286,36 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 2 : 0) sort_place_ke
   }
 }
 
-template <typename Id, int WARPS>
+template <typename Id, int WARPS, int BITS>
 static int sort_go(const SortArgs& a, cudaStream_t st) {
-  auto place = a.N <= 64 ? sort_place_kernel<Id, WARPS, 6> : sort_place_kernel<Id, WARPS, 10>;
-  const size_t smem = sort_smem(a.N, WARPS);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  auto place = sort_place_kernel<Id, WARPS, BITS>;
+  // the limit belongs to the kernel, not to the call (another thread's may be between this and its
+  // launch): what 2^BITS experts need, set once for a device
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sort_smem(1 << BITS, WARPS));
+    if (e != cudaSuccess) return cuda_status(e);
+    attr_set[dev] = true;
+  }
   const dim3 grid(a.chunks), block(WARPS * 32);
   if (a.chunks > 1) {
     const int r = launch_pdl(sort_count_kernel<Id>, grid, dim3(kCountThreads), sizeof(int) * (size_t)a.N, st, a);
     if (r != MOE_OK) return r;
   }
-  return launch_pdl(place, grid, block, smem, st, a);
+  return launch_pdl(place, grid, block, sort_smem(a.N, WARPS), st, a);
+}
+
+template <typename Id, int WARPS>
+static int sort_bits(const SortArgs& a, cudaStream_t st) {
+  return a.N <= 64 ? sort_go<Id, WARPS, 6>(a, st) : sort_go<Id, WARPS, 10>(a, st);
 }
 
 template <typename Id>
 static int sort_run(const SortArgs& a, int warps, cudaStream_t st) {
-  return warps == 16 ? sort_go<Id, 16>(a, st) : sort_go<Id, 32>(a, st);
+  return warps == 16 ? sort_bits<Id, 16>(a, st) : sort_bits<Id, 32>(a, st);
 }
 
 int launch_sort_slots(int T, int K, int N, const void* ids, int id_bytes, int32_t* counts, int32_t* offsets,
