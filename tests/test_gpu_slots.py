@@ -694,3 +694,40 @@ def test_sorts_of_two_threads():
         t.join()
     torch.cuda.synchronize()
     assert not failed, failed
+
+
+def test_more_pieces_than_an_index_holds():
+    """Narrow rows whose tokens times pieces pass 2^31: a piece is one element here."""
+    d, T = 63, 2 ** 31 // 63 + 1000
+    sr = torch.randperm(T, device="cuda").to(torch.int32).view(T, 1)
+    sr[::3] = -1
+    ys = torch.empty((T, d), dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.rand((T, 1), device="cuda") + 0.5
+    y = torch.full((T, d), 9.0, dtype=torch.bfloat16, device="cuda")
+
+    def check(at, out, src, weight):      # one product and one rounding: the same in any order
+        for a in range(0, T, 2 ** 22):
+            s, o = at[a:a + 2 ** 22, 0].long(), out[a:a + 2 ** 22]
+            has = (s >= 0)[:, None]
+            ref = src[s.clamp(min=0)].float() * weight[a:a + 2 ** 22]
+            assert torch.equal(o, torch.where(has, ref, 0.0).to(torch.bfloat16)), a
+
+    B.unpermute(ys, w, sr, y)
+    check(sr, y, ys, w)
+    ones = torch.ones_like(w)
+    B.permute_backward(ys, sr, y)
+    check(sr, y, ys, ones)
+    del y
+    # the copies, 31 single elements a row
+    d, T = 31, 2 ** 31 // 31 + 1000
+    x = torch.empty((T, d), dtype=torch.bfloat16, device="cuda").normal_()
+    sr = torch.randperm(T, device="cuda").to(torch.int32).view(T, 1)
+    back = torch.empty_like(sr)
+    back[sr[:, 0].long(), 0] = torch.arange(T, dtype=torch.int32, device="cuda")
+    del ys
+    xs = torch.zeros_like(x)
+    w, ones = torch.rand((T, 1), device="cuda") + 0.5, torch.ones((T, 1), device="cuda")
+    B.permute(x, sr, xs)
+    check(back, xs, x, ones)
+    B.unpermute_backward(x, None, w, sr, xs, None)
+    check(back, xs, x, w[back[:, 0].long()])

@@ -379,7 +379,7 @@ struct RowArgs {
   uint32_t* status;
   long long ldt, ldr, ldto, ldro, rows;
   int T, K, d;
-  int items;           // T * chunks: a warp's work is one chunk of one token
+  int items;           // T * chunks of a launch: a warp's (narrow rows: a thread's) work is one chunk of one token
   FastDiv chunks;      // chunks of a token: ceil(d / (32 V NV))
 };
 
@@ -764,14 +764,30 @@ __global__ void __launch_bounds__(kRowThreads) spread_dot_narrow_kernel(RowArgs 
 
 static unsigned blocks_for(long long n, int per_block) { return (unsigned)((n + per_block - 1) / per_block); }
 
-// Chunks per token and the grid over them; false when the index space is too large for any
-// buffer of this GPU's memory.
-static bool row_items(RowArgs& a, int chunk) {
-  const int n = (int)(((long long)a.d + chunk - 1) / chunk);
-  if ((long long)a.T * n >= (long long)INT_MAX) return false;
+template <typename P>
+static P* past(P* p, long long n) { return p ? p + n : p; }
+template <typename E>
+static void past_rows(const void*& p, long long n) { p = past(static_cast<const E*>(p), n); }
+template <typename E>
+static void past_rows(void*& p, long long n) { p = past(static_cast<E*>(p), n); }
+
+// Launches a kernel over the chunks of all tokens. They are numbered in 32 bits, so tokens with 2^31
+// chunks and more (narrow rows reach that: 34M tokens of 63 single elements) come in parts.
+template <typename E, typename Launch>
+static int over_tokens(RowArgs a, int chunk, Launch launch) {
+  const int n = (int)(((long long)a.d + chunk - 1) / chunk), most = INT_MAX / n;
   a.chunks = FastDiv((uint32_t)n);
-  a.items = a.T * n;
-  return true;
+  for (int left = a.T;;) {
+    a.T = std::min(left, most);
+    a.items = a.T * n;
+    const int r = launch(a);
+    left -= a.T;
+    if (r != MOE_OK || left == 0) return r;
+    past_rows<E>(a.tok, a.T * a.ldt);
+    past_rows<E>(a.tok_out, a.T * a.ldto);
+    a.w = past(a.w, (long long)a.T * a.K);
+    a.slot_row += (long long)a.T * a.K;
+  }
 }
 
 // Rows of at most this many pieces go to the narrow kernels, where a warp would leave half of its
@@ -782,14 +798,16 @@ template <int V>
 constexpr int kNarrow = V == 1 ? 64 : 32 * V;
 
 template <typename E, int V, int NV>
-static int collect_go(RowArgs a, cudaStream_t st) {
+static int collect_go(const RowArgs& a, cudaStream_t st) {
   if (a.d <= kNarrow<V>) {
-    if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
-    return launch_pdl(collect_narrow_kernel<E, V>, dim3(blocks_for(a.items, kRowThreads)), dim3(kRowThreads), 0,
-                      st, a);
+    return over_tokens<E>(a, V, [&](const RowArgs& p) {
+      return launch_pdl(collect_narrow_kernel<E, V>, dim3(blocks_for(p.items, kRowThreads)), dim3(kRowThreads), 0, st,
+                        p);
+    });
   }
-  if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
-  return launch_pdl(collect_kernel<E, V, NV>, dim3(blocks_for(a.items, kRowWarps)), dim3(kRowThreads), 0, st, a);
+  return over_tokens<E>(a, 32 * V * NV, [&](const RowArgs& p) {
+    return launch_pdl(collect_kernel<E, V, NV>, dim3(blocks_for(p.items, kRowWarps)), dim3(kRowThreads), 0, st, p);
+  });
 }
 
 template <typename E>
@@ -802,14 +820,16 @@ static int collect_run(const RowArgs& a, cudaStream_t st) {
 }
 
 template <typename E, int V, int NV>
-static int spread_go(RowArgs a, cudaStream_t st) {
+static int spread_go(const RowArgs& a, cudaStream_t st) {
   if (a.d <= (V == 1 ? 32 : kNarrow<V>)) {  // single elements: d = 63 39 us this way, about 23 by warps
-    if (!row_items(a, V)) return MOE_ERR_UNSUPPORTED;
-    return launch_pdl(spread_narrow_kernel<E, V>, dim3(blocks_for(a.items, kRowThreads)), dim3(kRowThreads), 0,
-                      st, a);
+    return over_tokens<E>(a, V, [&](const RowArgs& p) {
+      return launch_pdl(spread_narrow_kernel<E, V>, dim3(blocks_for(p.items, kRowThreads)), dim3(kRowThreads), 0, st,
+                        p);
+    });
   }
-  if (!row_items(a, 32 * V * NV)) return MOE_ERR_UNSUPPORTED;
-  return launch_pdl(spread_kernel<E, V, NV>, dim3(blocks_for(a.items, kRowWarps)), dim3(kRowThreads), 0, st, a);
+  return over_tokens<E>(a, 32 * V * NV, [&](const RowArgs& p) {
+    return launch_pdl(spread_kernel<E, V, NV>, dim3(blocks_for(p.items, kRowWarps)), dim3(kRowThreads), 0, st, p);
+  });
 }
 
 template <typename E, int V, int NV, bool CODES>
