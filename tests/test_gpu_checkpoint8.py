@@ -491,3 +491,74 @@ def test_a_checkpointed_backward_without_tokens_gives_zero_gradients(name):
                 assert bool(torch.isnan(g[n]).all()), n
             elif g[n] is not None:
                 assert int(torch.count_nonzero(g[n])) == 0, n
+
+
+# --------------------------------------------- more items than the grid takes in one sweep
+
+
+def power_of_two(e):
+    """2^e in 64 bits from its exponent's bits."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def stored_on_gpu(x):
+    """``stored_ref`` by blocks of all rows at once, in 64 bits on the GPU."""
+    val, byte = torch.empty(x.shape, dtype=torch.float64, device="cuda"), []
+    for c in range(0, x.shape[1], 32):
+        blk = x[:, c:c + 32].double()
+        m = blk.abs().amax(1)
+        E = torch.where(m > 0, torch.frexp(m)[1].double() - 7, -126.0).clamp(min=-126)   # frexp: m = f 2^e, f < 1
+        step = power_of_two(E)[:, None]
+        val[:, c:c + 32] = torch.round(blk / step).clamp(-127, 127) * step
+        byte.append((E + 127).to(torch.uint8))
+    return val, torch.stack(byte, 1)
+
+
+# (rows, columns, gap between the rows in elements). A sweep is 9472 items of eight blocks for single
+# elements, 1.2M items of 16 columns (store) and 2.4M of 16 bytes (restore) for strided 16-byte pieces.
+SWEEPS = [(20000, 1001, 0), (400003, 7, 0), (100001, 50, 1), (50001, 101, 0), (45001, 1000, 8), (45001, 1000, 0)]
+
+
+@pytest.mark.parametrize("rows,cols,pad", SWEEPS)
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_store_and_restore_in_many_sweeps(rows, cols, pad, dtype):
+    dt = TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn((rows, cols + pad), generator=g, device="cuda")
+    x = (x * torch.exp2(torch.randint(-9, 4, (rows, 1), generator=g, device="cuda"))).to(dt)[:, :cols]
+    for used in (rows, rows - 7):
+        n = torch.tensor([used], dtype=torch.int32, device="cuda")
+        codes = torch.full((rows, cols), 99, dtype=torch.int8, device="cuda")
+        scales = torch.full((rows, B.checkpoint8_scales(cols)), 77, dtype=torch.uint8, device="cuda")
+        B.checkpoint8(x, codes, scales, n)
+        val, byte = stored_on_gpu(x[:used])
+        assert torch.equal(scales[:used], byte)
+        step = power_of_two(byte.double() - 127).repeat_interleave(32, 1)[:, :cols]
+        assert torch.equal(codes[:used].double() * step, val)
+        assert bool((codes[used:] == 99).all()) and bool((scales[used:] == 77).all())
+        whole = torch.full((rows, cols + pad), 4.0, dtype=dt, device="cuda")
+        B.restore8(codes, scales, whole[:, :cols], n)
+        assert torch.equal(whole[:used, :cols].double(), val)
+        assert bool((whole[used:] == 4.0).all()) and bool((whole[:, cols:] == 4.0).all())
+
+
+@pytest.mark.parametrize("rows,F,packed", [(30000, 499, False), (200001, 33, False), (30001, 800, False),
+                                           (20001, 1024, True)])
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_swiglu_backward8_in_many_sweeps(rows, F, packed, pad):
+    """A sweep is 18944 items of 128 pairs for single elements and 9.7M pairs for 16-byte pieces."""
+    rng = np.random.default_rng(rows + F)
+    dt = torch.bfloat16
+    codes = torch.from_numpy(rng.integers(-127, 128, size=(rows, 2 * F)).astype(np.int8)).cuda()
+    scales = torch.from_numpy(rng.integers(107, 128, size=(rows, (2 * F + 31) // 32)).astype(np.uint8)).cuda()
+    flat = torch.randn((rows, F + pad), generator=torch.Generator(device="cuda").manual_seed(F), device="cuda").to(dt)
+    dh = flat[:, :F]
+    dz = torch.full((rows, 2 * F + pad), 9.0, dtype=dt, device="cuda")
+    h = torch.full((rows, F + pad), 9.0, dtype=dt, device="cuda")
+    n = torch.tensor([rows - 3], dtype=torch.int32, device="cuda")
+    B.swiglu_backward8(codes, scales, dh, dz[:, :2 * F], h[:, :F], packed=packed, rows_used=n)
+    for a in range(0, rows - 3, 5000):
+        r = slice(a, min(a + 5000, rows - 3))
+        check_swiglu(codes[r], scales[r], dh[r], dz[r, :2 * F], h[r, :F], packed)
+    for t, c in ((dz, 2 * F), (h, F)):
+        assert bool((t[rows - 3:] == 9.0).all()) and bool((t[:, c:] == 9.0).all())

@@ -731,3 +731,9 @@ def test_more_pieces_than_an_index_holds():
     check(back, xs, x, ones)
     B.unpermute_backward(x, None, w, sr, xs, None)
     check(back, xs, x, w[back[:, 0].long()])
+
+
+@pytest.mark.parametrize("T,K,N", [(262500, 8, 64), (150001, 16, 700)])
+def test_sort_of_several_passes_with_many_slots_in_the_last(T, K, N):
+    """Chunks of more slots than a CTA holds at once, the last pass with several a thread."""
+    check_sort(draw_ids(np.random.default_rng(T), T, K, N, 0.3), N)
