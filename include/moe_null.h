@@ -641,9 +641,9 @@ MOE_API int moe_unpermute(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t
                           int64_t ldys, const float* weights, const int32_t* slot_row, const void* base,
                           int64_t ldbase, void* y, int64_t ldy, void* status, moe_stream_t stream);
 
-/* Its gradient: dys[slot_row[t,k]] = weights[t,k] * dy[t] (one rounding) and dweights[t,k] =
- * <dy[t], ys[slot_row[t,k]]> in fp32 (0 for a slot without a row). base's gradient is dy.
- * dys may be NULL, or dweights and ys both. */
+/* Its gradient: dys[slot_row[t,k]] = weights[t,k] * dy[t] (an fp32 product, then one rounding to
+ * the type of dys) and dweights[t,k] = <dy[t], ys[slot_row[t,k]]> in fp32 (0 for a slot without
+ * a row). base's gradient is dy. dys may be NULL, or dweights and ys both. */
 MOE_API int moe_unpermute_backward(int32_t T, int32_t K, int64_t rows, int32_t d, int32_t dtype,
                                    const void* dy, int64_t lddy, const void* ys, int64_t ldys,
                                    const float* weights, const int32_t* slot_row, void* dys, int64_t lddys,
