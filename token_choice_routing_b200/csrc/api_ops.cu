@@ -11,7 +11,7 @@ static inline uint32_t* status_word(void* p) { return static_cast<uint32_t*>(p);
 
 constexpr int kMaxSlots = 32;          // slots of a token: one lane each
 constexpr int kMaxWidth = 1 << 30;     // columns of a row (column counters are 32-bit)
-constexpr int kMaxSortExperts = 1024;  // one thread per expert in the sort's scan
+constexpr int kMaxSortExperts = 1024;  // two per thread of the smaller CTA in the sort's scan, ids of ten bits
 
 static int check_slots(int32_t T, int32_t K) {
   if (T < 0 || K < 1) return MOE_ERR_INVALID_ARG;

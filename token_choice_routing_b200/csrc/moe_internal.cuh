@@ -202,6 +202,10 @@ int cuda_status(cudaError_t e);
 // pdl_wait() until its predecessor has completed and its writes are visible (a
 // no-op when the kernel was launched the ordinary way), and only then lets its
 // own successor start launching, so no kernel ever runs ahead of earlier work.
+// One does part of its work before it waits: sort_place_kernel reads and ranks the
+// ids. It may, because its direct predecessor (sort_count_kernel, always) does not
+// write them and lets it start only after its own wait, when whatever wrote the
+// ids had completed; it writes nothing to memory before it waits.
 template <typename... KArgs, typename... Args>
 inline int launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                       const Args&... args) {

@@ -48,7 +48,7 @@ __device__ __forceinline__ float elem_to_float<__half>(__half v) { return __half
 template <>
 __device__ __forceinline__ float elem_to_float<float>(float v) { return v; }
 
-// One rounding to nearest even, the only one an output of these kernels takes.
+// The rounding to an output's type, to nearest even, of a value computed in fp32.
 template <typename T>
 __device__ __forceinline__ T float_to_elem(float v);
 template <>
