@@ -1,5 +1,5 @@
-"""Whose buffers a layer call allocates when it is given a stream (no GPU: streams, kernels and the
-allocator's records are stood in for)."""
+"""Whose buffers a layer call allocates when it is given a stream, and the tensors that the checkpointed
+step refuses (no GPU: streams, kernels and the allocator's records are stood in for)."""
 import contextlib
 
 import pytest
@@ -38,10 +38,11 @@ def layer(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
     monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(B, "_device", lambda: -1)      # what get_device() gives for a CPU tensor
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.add((t.data_ptr(), s.cuda_stream)))
     for n in ("sort_slots", "permute", "permute_backward", "unpermute", "unpermute_backward", "expert_gate_up",
               "expert_down", "expert_ffn_backward", "clear_device_status", "forward", "backward",
-              "backward_checkpoint8"):
+              "forward_checkpoint8", "backward_checkpoint8"):
         monkeypatch.setattr(B, n, lambda *a, **k: None)
     m = object.__new__(MoENullLayer)
     m.d, m.N, m.M, m.K, m.F, m.F_shared, m.C, m.V = d, N, 2, K, F, F, 0, 0
@@ -80,3 +81,26 @@ def test_buffers_of_a_call_on_the_current_stream(layer, stream):
             if t is not None and t.numel():
                 assert layer.allocated[t.data_ptr()] == 1, (name, n)
     assert not layer.recorded
+
+
+def test_tokens_that_the_checkpointed_step_refuses(layer, monkeypatch):
+    """The library takes addresses: another type, width, layout or device would be read as bf16 rows."""
+    x = torch.zeros((T, d), dtype=torch.bfloat16)
+    out, ck = layer.alloc(T), layer.alloc_checkpoint8(T)
+    layer.forward_checkpoint8(x, None, out, ck)
+    layer.backward_checkpoint8(x, ck, x)
+    for bad in (x.float(), x[:, :64], x[:, :64].contiguous(), torch.zeros((d, T), dtype=torch.bfloat16).t(),
+                torch.zeros((T, 2 * d), dtype=torch.bfloat16)[:, ::2], x.view(torch.float16)):
+        with pytest.raises(ValueError):
+            layer.forward_checkpoint8(bad, None, out, ck)
+        with pytest.raises(ValueError):
+            layer.backward_checkpoint8(bad, ck, x)
+        with pytest.raises(ValueError):
+            layer.backward_checkpoint8(x, ck, bad)
+    with pytest.raises(ValueError):
+        layer.backward_checkpoint8(x, ck, x[:-1])
+    monkeypatch.setattr(B, "_device", lambda: 0)
+    with pytest.raises(ValueError):
+        layer.forward_checkpoint8(x, None, out, ck)
+    with pytest.raises(ValueError):
+        layer.backward_checkpoint8(x, ck, x)

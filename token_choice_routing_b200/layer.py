@@ -256,6 +256,13 @@ class MoENullLayer:
         B.backward(self.dims(T), self._weights, sv, dy, alpha, beta, g, grads["workspace"], stream)
         return grads
 
+    def _check_tokens(self, name: str, t: torch.Tensor, T: int):
+        if t.get_device() != B._device():
+            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, self.d) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bfloat16 of shape {(T, self.d)}, not {t.dtype} "
+                             f"{tuple(t.shape)}")
+
     # ------------------------------------------------------------ training with 8-bit checkpoints
 
     def alloc_checkpoint8(self, T: int) -> Dict[str, torch.Tensor]:
@@ -288,6 +295,7 @@ class MoENullLayer:
         may use; its buffers of the routing are left alone and the checkpoint's taken. Returns the
         outputs as ``forward`` does."""
         T = x.shape[0]
+        self._check_tokens("x", x, T)
         if out.get("xs") is None or out["xs"].shape[0] < T * self.K or out["y"].shape[0] < T:
             raise ValueError(f"an 8-bit checkpoint needs out from alloc({T}) with xs")
         if ck["slot_row"].shape[0] < T:
@@ -309,6 +317,8 @@ class MoENullLayer:
         gradients of the weights are zeros. grads: from ``alloc_grads(T, checkpoint8=True)``."""
         T = x.shape[0]
         dm = self.dims(T)
+        self._check_tokens("x", x, T)
+        self._check_tokens("dy", dy, T)
         if ck["slot_row"].shape[0] < T:
             raise ValueError(f"the checkpoint holds {ck['slot_row'].shape[0]} tokens, not {T}")
         if grads is None:
@@ -335,11 +345,6 @@ class MoENullLayer:
         dm = self.dims(T)
         dm.K, dm.M = K, max(self.M, K - self.N)  # the pool plays no part: only T, K and the real experts
         return dm
-
-    def _check_tokens(self, name: str, t: torch.Tensor, T: int):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, self.d) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bfloat16 of shape {(T, self.d)}, not {t.dtype} "
-                             f"{tuple(t.shape)}")
 
     def alloc_routed(self, T: int, K: int) -> Dict[str, torch.Tensor]:
         """Buffers of ``forward_routed`` for T tokens of K slots each."""
